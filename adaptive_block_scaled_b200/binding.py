@@ -73,6 +73,9 @@ def _load():
         "if4_linear_fused": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp],
         "if4_linear_quantized": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
                                  ctypes.c_size_t, _vp, _vp, _vp, _vp, _vp, _vp],
+        "nvfp4_linear_workspace_bytes": [_i64, _i64, _i64],
+        "nvfp4_linear": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_size_t,
+                         _vp, _int, _vp, _vp],
         "if6_quantize": [_vp, _int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp],
         "if3_quantize": [_vp, _int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp],
         "if6_dequantize": [_vp, _vp, _vp, _i64, _i64, _vp, _int, _i64, _vp],
@@ -89,6 +92,8 @@ def _load():
     lib.if4_status_str.restype = ctypes.c_char_p
     if hasattr(lib, "if4_linear_workspace_bytes"):
         lib.if4_linear_workspace_bytes.restype = ctypes.c_size_t
+    if hasattr(lib, "nvfp4_linear_workspace_bytes"):
+        lib.nvfp4_linear_workspace_bytes.restype = ctypes.c_size_t
     return lib
 
 
@@ -341,6 +346,71 @@ def if4_linear_quantized(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, works
                                     workspace.numel() * workspace.element_size(), _ptr(c),
                                     _ptr(c_codes), _ptr(c_scales), _ptr(c_ts), _ptr(err_flag),
                                     _stream(stream)), "if4_linear_quantized")
+
+
+# ------------------------------------------------- the NVFP4 linear layer ---
+
+def _device(name, *tensors):
+    """The CUDA device that every given tensor lives on (None entries skipped)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: every tensor must be on a CUDA device")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+        dev = t.device
+    return dev
+
+
+def _word(t, name, dtype):
+    if t is not None and (t.dtype != dtype or t.numel() < 1):
+        raise ValueError(f"{name} must be a {dtype} device tensor")
+
+
+def nvfp4_linear_workspace_bytes(M, N, K):
+    return int(lib.nvfp4_linear_workspace_bytes(int(M), int(N), int(K)))
+
+
+def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, err_flag,
+                 stream=None):
+    """C = A B^T of NVFP4 operands on the block-scaled tensor cores, into the
+    dense c [M, N] (bf16, f16 or f32).  workspace: a uint8 tensor of
+    nvfp4_linear_workspace_bytes, or None where that is 0."""
+    dev = _device("nvfp4_linear", a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
+                  err_flag)
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or c.dim() != 2:
+        raise ValueError("a_codes, b_codes and c must be 2-D")
+    M, K, N = a_codes.shape[0], a_codes.shape[1] * 2, b_codes.shape[0]
+    _u8(a_codes, "a_codes", (M, K // 2))
+    _u8(a_scales, "a_scales", (M, K // 16))
+    _u8(b_codes, "b_codes", (N, K // 2))
+    _u8(b_scales, "b_scales", (N, K // 16))
+    _word(a_ts, "a_ts", torch.float32)
+    _word(b_ts, "b_ts", torch.float32)
+    _word(err_flag, "err_flag", torch.int32)
+    if tuple(c.shape) != (M, N) or not c.is_contiguous():
+        raise ValueError(f"c must be a contiguous tensor of shape {(M, N)}")
+    with torch.cuda.device(dev):
+        _check(lib.nvfp4_linear(_ptr(a_codes), _ptr(a_scales), _ptr(a_ts), _ptr(b_codes),
+                                _ptr(b_scales), _ptr(b_ts), M, N, K, _ptr(workspace),
+                                0 if workspace is None else
+                                workspace.numel() * workspace.element_size(), _ptr(c),
+                                _dtype(c, "c"), _ptr(err_flag), _stream(stream)), "nvfp4_linear")
+
+
+def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
+    """a, b: (codes, scales, ts) of NVFP4 operands [M, K] and [N, K].  Returns
+    A B^T [M, N] of dtype."""
+    dev, M, N = a[0].device, a[0].shape[0], b[0].shape[0]
+    c = torch.empty((M, N), dtype=dtype, device=dev)
+    if err_flag is None:
+        err_flag = torch.zeros(1, dtype=torch.int32, device=dev)
+    need = nvfp4_linear_workspace_bytes(M, N, a[0].shape[1] * 2)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    nvfp4_linear(*a, *b, ws, c, err_flag, stream)
+    return c
 
 
 # ------------------------------------------------------- IF6 and IF3 ---

@@ -1,0 +1,1014 @@
+// NVFP4 x NVFP4 linear for B200 (sm_100a): C = A_hat B_hat^T straight from the
+// 4-bit codes, on the block-scaled tensor cores.
+//
+// With q the E2M1 values and s the E4M3 block scales of groups of 16 along K,
+//   C[m, n] = out( fl(a_ts * b_ts) * sum_g a_s[m, g] b_s[n, g] sum_{i<16} a_q[m, 16 g + i] b_q[n, 16 g + i] ).
+// tcgen05.mma kind::mxf4nvf4 with a scale per 16 elements evaluates the double
+// sum from the codes as they are stored (two per byte, the first in the low
+// nibble, K contiguous) and the scale bytes as UE4M3, accumulating in binary32
+// in tensor memory: no operand is decoded, and a step of K = 64 takes the time
+// that K = 16 takes in fp16.
+//
+// What the codes' row-major scale layout costs: the MMA reads the scales of
+// one K step of 64 from tensor memory, the 4 bytes of operand row m in lane
+// m % 32 of column m / 32.  tcgen05.cp (32x128b, repeated for the four lane
+// quarters) fills that from 512 contiguous bytes of shared memory, row m's 4
+// bytes at (m % 32) * 16 + (m / 32) * 4.  The scales of a row lie K / 16
+// bytes apart from the next row's, so no tiled copy makes this order from
+// them: scale warps load 16 bytes per row and 256 of K into registers and
+// store them as four words, one per K step.  They work in units of 512 of K,
+// so that the two lanes of a row use a whole 32-byte sector.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/if4.h"
+#include "if4_device.cuh"
+#include "if4_tc.cuh"
+
+namespace {
+
+using namespace if4dev;
+
+constexpr int SK = 256;               // K per stage: 128 bytes of codes, one swizzle row
+constexpr int MMA_K = 64;             // K per tcgen05.mma of 4-bit operands
+constexpr int KSTEPS = SK / MMA_K;
+constexpr int UNIT = 2 * SK;          // K per unit of the scale ring
+constexpr int SF_STEP = 512;          // scale bytes of 128 rows x one K step
+constexpr int SF_BLOCK = KSTEPS * SF_STEP;   // 128 rows x one stage
+
+// instruction descriptor, kind::mxf4nvf4: A and B E2M1 (1), both K-major,
+// UE4M3 scales (bit 23 clear), scale ids 0, K = 64
+__host__ __device__ constexpr uint32_t mxf4_idesc(int m, int n)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Shared-memory descriptor of one 512-byte scale block for tcgen05.cp: four
+// 8-row groups of 16-byte rows, 128 bytes apart, not swizzled.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
+
+// The issuing warp stays converged and one elected lane issues: the operands
+// of tcgen05 instructions are then warp-uniform values that the compiler keeps
+// in uniform registers.  With one lane in a branch of its own the 16
+// instructions of a stage took twice the MMAs' time (124 against 63 us at
+// 8192 x 4096 x 4096 with the copies of codes and scales left out).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
+// mbar_wait by a whole warp, with one answer for all its lanes.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    return __all_sync(0xFFFFFFFFu, mbar_wait<CLUSTER>(bar, parity, abort_flag));
+}
+
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t d)
+{
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(d));
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(d));
+}
+
+template <int CG>
+__device__ __forceinline__ void umma_nvfp4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t accumulate)
+{
+    if constexpr (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+                     " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                     :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb),
+                        "r"(accumulate));
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+                     " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                     :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb),
+                        "r"(accumulate));
+}
+
+__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.b32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void fence_async_smem()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// The 16 scale bytes at p, of which the first nb exist (nb <= 0: none); the
+// others read as 0.  VEC: the bytes that p's and nb's alignment allows per
+// load: 16 (K % 256 == 0, aligned base), 4 (K % 64 == 0) or 2 (K % 32 == 0).
+template <int VEC>
+__device__ __forceinline__ void load_scales16(const uint8_t *p, int nb, uint32_t (&w)[4])
+{
+    w[0] = w[1] = w[2] = w[3] = 0u;
+    if constexpr (VEC == 16) {
+        if (nb > 0)
+            asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    } else if constexpr (VEC == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (nb > 4 * j)
+                asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[j]) : "l"(p + 4 * j));
+    } else {
+        uint16_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            h[j] = 0;
+            if (nb > 2 * j)
+                asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h[j]) : "l"(p + 2 * j));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)h[2 * j] | (uint32_t)h[2 * j + 1] << 16;
+    }
+}
+
+// One accumulator value to its output type.
+template <int ODT>
+__device__ __forceinline__ void store_c(void *c, int64_t i, float v)
+{
+    if constexpr (ODT == IF4_F32) {
+        static_cast<float *>(c)[i] = v;
+    } else if constexpr (ODT == IF4_BF16) {
+        static_cast<__nv_bfloat16 *>(c)[i] = __float2bfloat16_rn(v);
+    } else {
+        static_cast<__half *>(c)[i] = __float2half_rn(v);
+    }
+}
+
+// ------------------------------------------------- few rows: split over K ----
+//
+// Few tokens, or few output tiles.  The weight rows take the MMA's M side (128
+// per CTA) and NT tokens its N side, so D is C transposed: a lane holds one
+// output column and a warp's stores are contiguous along N.  A cluster of S
+// CTAs splits K into whole units; each CTA leaves its binary32 partial tile in
+// its shared memory, and the CTAs add the S partials in rank order through
+// distributed shared memory, each for its share of the tokens: no workspace,
+// no atomics, the same sum every time.
+
+namespace split {
+
+constexpr int WR = 128;                        // weight rows per CTA
+constexpr int W_BYTES = WR * SK / 2;           // 16 KB per stage
+constexpr int THREADS = 192;                   // TMA, MMA, four scale / epilogue warps
+constexpr int SF_UNITS = 3;
+constexpr int SF_UNIT_BYTES = 4 * SF_BLOCK;    // two stages x (weights, tokens)
+constexpr int SF_COLS = 2 * 2 * KSTEPS * 4;    // two stages of scale columns
+
+template <int NT>
+struct Cfg {
+    static constexpr int X_BYTES = NT * SK / 2;
+    static constexpr int STAGE = W_BYTES + X_BYTES;
+    // up to 32 tokens: two CTAs of 106-116 KB per SM; above: one per SM
+    static constexpr int STAGES = NT <= 16 ? 4 : NT <= 32 ? 4 : NT <= 64 ? 7 : 6;
+    static constexpr int SF_OFF = STAGES * STAGE;
+    static constexpr int BAR_OFF = SF_OFF + SF_UNITS * SF_UNIT_BYTES;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+    static constexpr int TMEM_COLS = NT + SF_COLS <= 128 ? 128 : 256;
+    static_assert(NT * WR * 4 <= SF_OFF, "the partial tile fits the stages");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+}  // namespace split
+
+template <int NT, int VEC, int ODT>
+__global__ void __launch_bounds__(split::THREADS, 1)
+nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
+                   const __grid_constant__ CUtensorMap tmap_x,
+                   const uint8_t *__restrict__ w_scales, const uint8_t *__restrict__ x_scales,
+                   const float *__restrict__ w_ts, const float *__restrict__ x_ts,
+                   void *__restrict__ c, int M, int N, int K, int *err)
+{
+    using namespace split;
+    using C = Cfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem_w = smem;
+    uint8_t *smem_x = smem + C::STAGES * W_BYTES;
+    uint8_t *smem_sf = smem + C::SF_OFF;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + C::STAGES;
+    uint64_t *sf_full = empty + C::STAGES;
+    uint64_t *sf_empty = sf_full + SF_UNITS;
+    uint64_t *acc_full = sf_empty + SF_UNITS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);   // warp-uniform
+    const int lane = threadIdx.x & 31;
+    uint32_t ranks;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    const uint32_t rank = cta_rank();
+    const int n0 = blockIdx.y * WR;
+    const int m0 = blockIdx.z * NT;
+    const int units = (K + UNIT - 1) / UNIT;
+    const int u0 = (int)((int64_t)units * rank / ranks);
+    const int u1 = (int)((int64_t)units * (rank + 1) / ranks);
+    const int kb0 = u0 * 2;                                  // stages of this CTA
+    const int kb1 = min(u1 * 2, (K + SK - 1) / SK);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < SF_UNITS; ++s) {
+            mbar_init(smem_u32(&sf_full[s]), 128);
+            mbar_init(smem_u32(&sf_empty[s]), 1);
+        }
+        mbar_init(smem_u32(acc_full), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tmap_w);
+        prefetch_tmap(&tmap_x);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tmem_slot)), "r"(C::TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // programmatic launch: nothing above reads a kernel input
+    pdl_enter();
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------- TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) break;
+            const uint32_t fb = smem_u32(&full[stage]);
+            mbar_expect_tx(fb, C::STAGE);
+            tma_load_2d(smem_u32(smem_w + stage * W_BYTES), &tmap_w, kb * (SK / 2), n0, fb);
+            tma_load_2d(smem_u32(smem_x + stage * C::X_BYTES), &tmap_x, kb * (SK / 2), m0, fb);
+            ++issued;
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+        }
+        // every copy issued here lands before the shared memory is reused or
+        // the CTA exits (bounded)
+        const int pending = issued < C::STAGES ? issued : C::STAGES;
+        for (int i = 0; i < pending; ++i) {
+            if (--stage < 0) { stage = C::STAGES - 1; phase ^= 1u; }
+            const unsigned long long t0 = globaltimer();
+            while (!mbar_try_wait(smem_u32(&full[stage]), phase))
+                if (globaltimer() - t0 > WAIT_LIMIT_NS) break;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer
+        const bool issue = elect_one();
+        const uint64_t w_desc = smem_desc_sw128(smem_u32(smem_w));
+        const uint64_t x_desc = smem_desc_sw128(smem_u32(smem_x));
+        const uint64_t sf_desc = smem_desc_scales(smem_u32(smem_sf));
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, sf_phase = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const int half = (kb - kb0) & 1;
+            if (half == 0 && !warp_wait(smem_u32(&sf_full[slot]), sf_phase, abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t wd = w_desc + (uint64_t)(stage * (W_BYTES >> 4));
+            const uint64_t xd = x_desc + (uint64_t)(stage * (C::X_BYTES >> 4));
+            const uint64_t sd = sf_desc + (uint64_t)((slot * SF_UNIT_BYTES + half * SF_BLOCK) >> 4);
+            const uint32_t tsf = tmem_base + NT + half * (SF_COLS / 2);
+            const int steps = min(KSTEPS, (K - kb * SK + MMA_K - 1) / MMA_K);
+            if (issue) {
+#pragma unroll
+                for (int kk = 0; kk < KSTEPS; ++kk) {
+                    if (kk < steps) {
+                        const uint32_t tw = tsf + kk * 4, tx = tsf + 16 + kk * 4;
+                        copy_scales<1>(tw, sd + kk * (SF_STEP >> 4));
+                        copy_scales<1>(tx, sd + ((2 * SF_BLOCK + kk * SF_STEP) >> 4));
+                        umma_nvfp4<1>(tmem_base, wd + 2 * kk, xd + 2 * kk, mxf4_idesc(WR, NT), tw,
+                                      tx, kb != kb0 || kk != 0 ? 1u : 0u);
+                    }
+                }
+                umma_commit(smem_u32(&empty[stage]));
+                if (half == 1) umma_commit(smem_u32(&sf_empty[slot]));
+            }
+            __syncwarp();
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+            if (half == 1 && ++slot == SF_UNITS) { slot = 0; sf_phase ^= 1u; }
+        }
+        // MMAs and scale copies complete before anyone reads the accumulator,
+        // reuses the shared memory or frees tensor memory
+        if (issue) {
+            umma_commit(smem_u32(acc_full));
+            if (!ok) {
+                const unsigned long long t0 = globaltimer();
+                while (!mbar_try_wait(smem_u32(acc_full), 0))
+                    if (globaltimer() - t0 > WAIT_LIMIT_NS) break;
+            }
+        }
+    } else if (warp >= 2) {
+        // ---------------------------------------------------- block scales
+        // thread t: chunk t & 1 (one stage) of rows 32 p + 16 i + 4 v + q
+        const int t = threadIdx.x - 64;
+        const int ch = t & 1, q = (t >> 1) & 3, p = (t >> 3) & 3, v = t >> 5;
+        const int row0 = 32 * p + 4 * v + q;                 // and row0 + 16
+        const int kg = K / 16;
+        const uint32_t so = (uint32_t)((row0 & 31) * 16 + p * 4);
+        int slot = 0;
+        uint32_t phase = 0;
+        uint32_t bad = 0;
+        uint32_t ww[2][4], xw[2][4];
+        auto fetch = [&](int u) {
+            const int g0 = u * (UNIT / 16) + ch * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = row0 + 16 * i;
+                load_scales16<VEC>(w_scales + (int64_t)(n0 + r) * kg + g0,
+                                   n0 + r < N ? kg - g0 : 0, ww[i]);
+                if (r < NT)
+                    load_scales16<VEC>(x_scales + (int64_t)(m0 + r) * kg + g0,
+                                       m0 + r < M ? kg - g0 : 0, xw[i]);
+            }
+        };
+        if (u0 < u1) fetch(u0);
+        for (int u = u0; u < u1; ++u) {
+            if (!mbar_wait(smem_u32(&sf_empty[slot]), phase ^ 1u, abort_flag)) break;
+            const uint32_t d = smem_u32(smem_sf + slot * SF_UNIT_BYTES) + ch * SF_BLOCK + so;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sts_u32(d + i * 256 + j * SF_STEP, ww[i][j]);
+                    bad |= ww[i][j];
+                }
+                if (row0 + 16 * i < NT) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sts_u32(d + 2 * SF_BLOCK + i * 256 + j * SF_STEP, xw[i][j]);
+                        bad |= xw[i][j];
+                    }
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(smem_u32(&sf_full[slot]));
+            if (++slot == SF_UNITS) { slot = 0; phase ^= 1u; }
+            if (u + 1 < u1) fetch(u + 1);
+        }
+        if ((bad & 0x80808080u) && err) atomicOr(err, IF4_DEV_BAD_SCALE);
+        // -------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(acc_full), 0, abort_flag));
+        tc_fence_after();
+        if (ok && u0 < u1) {
+            const float scale = __fmul_rn(*x_ts, *w_ts);
+            float *part = reinterpret_cast<float *>(smem);
+#pragma unroll 1
+            for (int mc = 0; mc < NT && m0 + mc < M; mc += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)mc, r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int m = m0 + mc + j;
+                    if (ranks > 1)
+                        part[(mc + j) * WR + row] = __uint_as_float(r[j]);
+                    else if (m < M && n0 + row < N)
+                        store_c<ODT>(c, (int64_t)m * N + n0 + row,
+                                     __fmul_rn(__uint_as_float(r[j]), scale));
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (ranks > 1) {
+        cluster_sync();
+        if (warp >= 2 && !*abort_flag) {
+            const int row = (warp & 3) * 32 + lane;
+            const float scale = __fmul_rn(*x_ts, *w_ts);
+            const uint32_t part = smem_u32(smem);
+            if (n0 + row < N)
+                for (int m = rank; m < NT && m0 + m < M; m += ranks) {
+                    float sum = 0.0f;
+                    for (uint32_t s = 0; s < ranks; ++s) {
+                        float v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(v) : "r"(map_to(part + (m * WR + row) * 4, s))
+                                     : "memory");
+                        sum = __fadd_rn(sum, v);
+                    }
+                    store_c<ODT>(c, (int64_t)(m0 + m) * N + n0 + row, __fmul_rn(sum, scale));
+                }
+        }
+        cluster_sync();                  // no CTA leaves while another reads its partials
+    }
+    if (threadIdx.x == 0 && *abort_flag && err) atomicOr(err, IF4_DEV_TIMEOUT);
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                     :: "r"(tmem_base), "r"(C::TMEM_COLS));
+    }
+}
+
+// --------------------------------------------------- many rows: CTA pairs ----
+//
+// A pair of CTAs on two SMs computes 256 x 256 tiles with tcgen05.mma of
+// cta_group::2, persistent over the tiles: CTA r holds rows r * 128..+127 of
+// A's slab and half of B's, the leader's MMAs read both halves, and each CTA
+// keeps its own 128 rows of the product.  The MMA reads a row's scales from
+// the tensor memory of the CTA that holds the accumulator, so each CTA brings
+// the scales of its own A rows and of all 256 B rows.
+//
+// Scales: a small kernel first puts both operands' scales into the workspace
+// in the order that tcgen05.cp reads (pack_scales), so that here they are two
+// more tiles of the stage's TMA copies.  Loading and reordering them in this
+// kernel instead (four warps, a second ring) was measured at 8192 x 4096 x
+// 4096: 135 us, the ring's round trips and the loads' latency in the way of
+// every stage.
+//
+// Tensor memory: two accumulators of 256 columns and the scales' 48 do not fit
+// 512 columns, and narrower tiles read A's shared memory more often per
+// column: without stores 40.9 us for 256 columns, 49.5 for 224, 56.0 for 192.
+// So the accumulators overlap in OVERLAP columns: the epilogue first takes the
+// overlap to registers and releases it, and the next tile's MMAs run under the
+// rest.
+
+namespace duo {
+
+constexpr int PM = 128;                        // rows per CTA
+constexpr int BN = 256;                        // columns per pair
+constexpr int A_BYTES = PM * SK / 2;           // 16 KB per stage
+constexpr int B_BYTES = BN / 2 * SK / 2;       // 16 KB
+constexpr int SFA_BYTES = SF_BLOCK;            // 2 KB
+constexpr int SFB_BYTES = 2 * SF_BLOCK;        // 4 KB: two blocks of 128 rows
+constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int STAGES = 5;
+constexpr int THREADS = 192;                   // TMA, MMA, 4 epilogue warps
+constexpr int SF_COLS = 3 * KSTEPS * 4;        // scale columns of a stage
+constexpr int OVERLAP = 2 * BN + SF_COLS - 512;   // 48
+constexpr int ACC1 = BN - OVERLAP;             // first column of the second accumulator
+constexpr int SF_COL0 = 512 - SF_COLS;
+constexpr int BAR_OFF = STAGES * STAGE;
+constexpr int SMEM = BAR_OFF + 256 + 1024;
+static_assert(SMEM <= 227 * 1024, "shared memory");
+static_assert(ACC1 + BN <= SF_COL0 && OVERLAP == 48, "tensor memory");
+
+}  // namespace duo
+
+// The scales of one operand: [rows, K / 16] as stored, and [row blocks of 128]
+// [K steps of 64, a multiple of 4][512 bytes] as tcgen05.cp reads them.
+struct ScalePack {
+    const uint8_t *src;
+    uint8_t *dst;
+    int rows;
+};
+
+// A thread takes one stage (four K steps) of the rows m, m + 32, m + 64 and
+// m + 96 of a block, 16 bytes each, and writes their words as four 16-byte
+// lines, one per K step.  Rows and K past the end become 0.  A warp covers 16
+// rows m x 2 stages: whole 32-byte sectors read, 256-byte runs written.
+template <int VEC>
+__global__ void __launch_bounds__(256)
+pack_scales(ScalePack a, ScalePack b, int K, int *err)
+{
+    pdl_enter();
+    const int kg = K / 16, stages = (K + SK - 1) / SK, pairs = (stages + 1) / 2;
+    const int64_t na = (int64_t)((a.rows + 127) / 128) * pairs * 2;   // warps' work items
+    const int64_t nb = (int64_t)((b.rows + 127) / 128) * pairs * 2;
+    const int lane = threadIdx.x & 31;
+    uint32_t bad = 0;
+    for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < na + nb;
+         w += (int64_t)gridDim.x * 8) {
+        const bool first = w < na;
+        const uint8_t *src = first ? a.src : b.src;
+        uint8_t *dst = first ? a.dst : b.dst;
+        const int rows = first ? a.rows : b.rows;
+        const int64_t i = first ? w : w - na;
+        const int m = (int)(i & 1) * 16 + (lane >> 1);
+        const int64_t pr = i >> 1;
+        const int stage = (int)(pr % pairs) * 2 + (lane & 1);
+        const int64_t block = pr / pairs;
+        if (stage >= stages) continue;
+        uint32_t v[4][4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int64_t row = block * 128 + m + 32 * p;
+            load_scales16<VEC>(src + row * kg + stage * 16, row < rows ? kg - stage * 16 : 0, v[p]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bad |= v[p][j];
+        }
+        uint8_t *d = dst + ((block * stages + stage) * KSTEPS) * SF_STEP + m * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st_v4(d + j * SF_STEP, v[0][j], v[1][j], v[2][j], v[3][j]);
+    }
+    if ((bad & 0x80808080u) && err) atomicOr(err, IF4_DEV_BAD_SCALE);
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                                 int z, uint32_t bar_cluster)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z),
+                    "r"(bar_cluster)
+                 : "memory");
+}
+
+// N accumulator columns (16 or 32) of one row, scaled, to C's type.  width:
+// bytes that C's alignment and N allow per store (32, 16 or less)
+template <int ODT, int COLS>
+__device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float scale, int row, int M,
+                                           int N, int col0, int width)
+{
+    if (row >= M) return;
+    const int64_t base = (int64_t)row * N + col0;
+    constexpr int ES = ODT == IF4_F32 ? 4 : 2;
+    if (width >= 16 && col0 + COLS <= N) {
+        uint32_t w[COLS * ES / 4];
+#pragma unroll
+        for (int i = 0; i < COLS; i += 2) {
+            const float lo = __fmul_rn(__uint_as_float(r[i]), scale);
+            const float hi = __fmul_rn(__uint_as_float(r[i + 1]), scale);
+            if constexpr (ODT == IF4_F32) {
+                w[i] = __float_as_uint(lo);
+                w[i + 1] = __float_as_uint(hi);
+            } else {
+                w[i / 2] = ODT == IF4_BF16 ? bf16x2_from_f32(lo, hi) : f16x2_from_f32(lo, hi);
+            }
+        }
+        uint8_t *p = static_cast<uint8_t *>(c) + base * ES;
+        if (width == 32) {
+#pragma unroll
+            for (int q = 0; q < COLS * ES / 32; ++q) {
+                const uint32_t(&x)[8] = *reinterpret_cast<const uint32_t(*)[8]>(w + 8 * q);
+                st_v8(p + 32 * q, x);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < COLS * ES / 16; ++q)
+                st_v4(p + 16 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i)
+            if (col0 + i < N)
+                store_c<ODT>(c, base + i, __fmul_rn(__uint_as_float(r[i]), scale));
+    }
+}
+
+template <int ODT>
+__global__ void __launch_bounds__(duo::THREADS, 1)
+nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
+                  const __grid_constant__ CUtensorMap tmap_b,
+                  const __grid_constant__ CUtensorMap tmap_sa,
+                  const __grid_constant__ CUtensorMap tmap_sb,
+                  const float *__restrict__ a_ts, const float *__restrict__ b_ts,
+                  void *__restrict__ c, int M, int N, int K, int *err)
+{
+    using namespace duo;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem_a = smem;
+    uint8_t *smem_b = smem_a + STAGES * A_BYTES;
+    uint8_t *smem_sa = smem_b + STAGES * B_BYTES;
+    uint8_t *smem_sb = smem_sa + STAGES * SFA_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + BAR_OFF);   // leader
+    uint64_t *empty = full + STAGES;               // both
+    uint64_t *acc_full = empty + STAGES;           // both
+    uint64_t *acc_free = acc_full + 2;             // leader: the overlap is free
+    uint64_t *drain = acc_free + 1;                // leader
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);   // warp-uniform
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const bool leader = rank == 0;
+    const int m_tiles = (M + 2 * PM - 1) / (2 * PM);
+    const int tiles = m_tiles * ((N + BN - 1) / BN);
+    const int pair_id = blockIdx.x >> 1;
+    const int num_pairs = gridDim.x >> 1;
+    const int k_blocks = (K + SK - 1) / SK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(&acc_full[0]), 1);
+        mbar_init(smem_u32(&acc_full[1]), 1);
+        mbar_init(smem_u32(acc_free), 2 * 4);
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tmap_a);
+        prefetch_tmap(&tmap_b);
+        prefetch_tmap(&tmap_sa);
+        prefetch_tmap(&tmap_sb);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tmem_slot)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                      // peer barriers initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // programmatic launch: nothing above reads a kernel input
+    pdl_enter();
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------- TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = pair_id; t < tiles && ok; t += num_pairs) {
+            const int mt = t % m_tiles, nt = t / m_tiles;
+            const int m0 = mt * 2 * PM + (int)rank * PM;
+            const int n0 = nt * BN + (int)rank * (BN / 2);
+            for (int kb = 0; kb < k_blocks; ++kb) {
+                if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) { ok = false; break; }
+                const uint32_t fb = map_to(smem_u32(&full[stage]), 0);
+                if (leader) mbar_expect_tx(smem_u32(&full[stage]), 2 * STAGE);
+                tma_load_2d_pair(smem_u32(smem_a + stage * A_BYTES), &tmap_a, kb * (SK / 2), m0, fb);
+                tma_load_2d_pair(smem_u32(smem_b + stage * B_BYTES), &tmap_b, kb * (SK / 2), n0, fb);
+                tma_load_3d_pair(smem_u32(smem_sa + stage * SFA_BYTES), &tmap_sa, 0, kb * KSTEPS,
+                                 mt * 2 + (int)rank, fb);
+                tma_load_3d_pair(smem_u32(smem_sb + stage * SFB_BYTES), &tmap_sb, 0, kb * KSTEPS,
+                                 nt * 2, fb);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+        // every copy issued here has been consumed by the leader's MMAs when
+        // the loops end normally; after an abort, give them a bounded time
+        const unsigned long long t0 = globaltimer();
+        if (*abort_flag)
+            while (globaltimer() - t0 < 2000000ull) { }
+    } else if (warp == 1 && leader) {
+        // ------------------------------------------- MMA issuer (leader)
+        const bool issue = elect_one();
+        const uint64_t a_desc = smem_desc_sw128(smem_u32(smem_a));
+        const uint64_t b_desc = smem_desc_sw128(smem_u32(smem_b));
+        const uint64_t sa_desc = smem_desc_scales(smem_u32(smem_sa));
+        const uint64_t sb_desc = smem_desc_scales(smem_u32(smem_sb));
+        const uint32_t ta0 = tmem_base + SF_COL0, tb0 = ta0 + KSTEPS * 4;
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, free_phase = 1;
+        bool ok = true;
+        for (int t = pair_id; t < tiles && ok; t += num_pairs) {
+            // the previous tile's epilogue holds the overlap until it says so
+            if (!warp_wait<true>(smem_u32(acc_free), free_phase, abort_flag)) break;
+            free_phase ^= 1u;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC1);
+            for (int kb = 0; kb < k_blocks; ++kb) {
+                if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t ad = a_desc + (uint64_t)(stage * (A_BYTES >> 4));
+                const uint64_t bd = b_desc + (uint64_t)(stage * (B_BYTES >> 4));
+                const uint64_t sad = sa_desc + (uint64_t)(stage * (SFA_BYTES >> 4));
+                const uint64_t sbd = sb_desc + (uint64_t)(stage * (SFB_BYTES >> 4));
+                const int steps = min(KSTEPS, (K - kb * SK + MMA_K - 1) / MMA_K);
+                if (issue) {
+#pragma unroll
+                    for (int kk = 0; kk < KSTEPS; ++kk) {
+                        if (kk < steps) {
+                            const uint32_t ta = ta0 + kk * 4, tb = tb0 + kk * 8;
+                            copy_scales<2>(ta, sad + kk * (SF_STEP >> 4));
+                            copy_scales<2>(tb, sbd + kk * (SF_STEP >> 4));
+                            copy_scales<2>(tb + 4, sbd + ((SF_BLOCK + kk * SF_STEP) >> 4));
+                            umma_nvfp4<2>(d_tmem, ad + 2 * kk, bd + 2 * kk, mxf4_idesc(2 * PM, BN),
+                                          ta, tb, (kb | kk) != 0 ? 1u : 0u);
+                        }
+                    }
+                    umma_commit_both(smem_u32(&empty[stage]));
+                    if (kb + 1 == k_blocks) umma_commit_both(smem_u32(&acc_full[acc]));
+                }
+                __syncwarp();
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            acc ^= 1;
+        }
+        if (issue) {
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                         :: "r"(smem_u32(drain)) : "memory");
+            const unsigned long long t0 = globaltimer();
+            while (!mbar_try_wait(smem_u32(drain), 0))
+                if (globaltimer() - t0 > WAIT_LIMIT_NS) break;
+        }
+    } else if (warp >= 2) {
+        // -------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        const float scale = __fmul_rn(*a_ts, *b_ts);
+        constexpr int ES = ODT == IF4_F32 ? 4 : 2;
+        const uintptr_t al = reinterpret_cast<uintptr_t>(c) | (uintptr_t)((int64_t)N * ES);
+        const int width = al % 32 == 0 ? 32 : al % 16 == 0 ? 16 : 0;
+        const uint32_t free_bar = map_to(smem_u32(acc_free), 0);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int t = pair_id; t < tiles; t += num_pairs) {
+            const int row = (t % m_tiles) * 2 * PM + (int)rank * PM + quarter * 32 + lane;
+            const int n0 = (t / m_tiles) * BN;
+            if (!warp_wait(smem_u32(&acc_full[acc]), acc_phase, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
+            // the overlap: the first accumulator's last 48 columns, the
+            // second's first 48
+            const int c0 = acc ? 0 : ACC1;
+            const int rest = acc ? OVERLAP : 0;
+            uint32_t r[32], q[16];
+            tmem_ld32(lanes + ACC1, r);
+            tmem_ld16(lanes + ACC1 + 32, q);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(free_bar);
+            store_cols<ODT, 32>(c, r, scale, row, M, N, n0 + c0, width);
+            store_cols<ODT, 16>(c, q, scale, row, M, N, n0 + c0 + 32, width);
+            const uint32_t base = lanes + (uint32_t)(acc * ACC1 + rest);
+#pragma unroll 1
+            for (int ch = 0; ch < ACC1 / 32; ++ch) {
+                tmem_ld32(base + ch * 32, r);
+                store_cols<ODT, 32>(c, r, scale, row, M, N, n0 + rest + ch * 32, width);
+            }
+            tmem_ld16(base + ACC1 / 32 * 32, q);
+            store_cols<ODT, 16>(c, q, scale, row, M, N, n0 + rest + ACC1 / 32 * 32, width);
+            acc_phase ^= (uint32_t)acc;
+            acc ^= 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                      // the peer's MMAs and copies are done
+    if (threadIdx.x == 0 && *abort_flag && err) atomicOr(err, IF4_DEV_TIMEOUT);
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                     :: "r"(tmem_base), "r"(512));
+    }
+}
+
+// ------------------------------------------------------------ host side ----
+
+constexpr int MAX_DEVICES = 64;
+constexpr int64_t MAX_MN = 1 << 22, MAX_K = 1 << 20;
+
+// What a launch needs to know of the current device, read once per device.
+struct Device {
+    int id, sms;
+};
+
+int current_device(Device &d)
+{
+    static std::once_flag once[MAX_DEVICES];
+    static int sms[MAX_DEVICES], rcs[MAX_DEVICES];
+    if (cudaGetDevice(&d.id) != cudaSuccess || d.id < 0 || d.id >= MAX_DEVICES) return IF4_ERR_CUDA;
+    const int id = d.id;
+    std::call_once(once[id], [id] { rcs[id] = sm_count_checked(sms[id]); });
+    d.sms = sms[id];
+    return rcs[id];
+}
+
+// Codes [rows, K / 2] -> tensor map with a (128 bytes x box_rows) box.
+bool make_codes_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+    const cuuint32_t box[2] = {(cuuint32_t)(SK / 2), (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Problem {
+    const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
+    const float *a_ts, *b_ts;
+    int64_t M, N, K;
+    void *workspace;
+    void *c;
+    int *err;
+    cudaStream_t st;
+};
+
+// The kernel's shared-memory limit is raised once per device and kernel.
+template <typename Kernel>
+int allow_smem(Kernel kernel, int bytes, const Device &d, std::once_flag (&once)[MAX_DEVICES],
+               cudaError_t (&rcs)[MAX_DEVICES])
+{
+    std::call_once(once[d.id], [&] {
+        rcs[d.id] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return rcs[d.id] == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
+}
+
+template <int NT, int VEC, int ODT>
+int launch_split(const Problem &p, const Device &d, int ranks)
+{
+    using C = split::Cfg<NT>;
+    auto kernel = nvfp4_linear_split<NT, VEC, ODT>;
+    static std::once_flag once[MAX_DEVICES];
+    static cudaError_t rcs[MAX_DEVICES];
+    const int rc = allow_smem(kernel, C::SMEM, d, once, rcs);
+    if (rc != IF4_OK) return rc;
+    CUtensorMap mw, mx;
+    if (!make_codes_map(&mw, p.b_codes, p.N, p.K, split::WR) ||
+        !make_codes_map(&mx, p.a_codes, p.M, p.K, NT))
+        return IF4_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ranks, (unsigned)((p.N + split::WR - 1) / split::WR),
+                       (unsigned)((p.M + NT - 1) / NT));
+    cfg.blockDim = dim3(split::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = p.st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, mw, mx, p.b_scales, p.a_scales, p.b_ts, p.a_ts, p.c,
+                           (int)p.M, (int)p.N, (int)p.K, p.err) != cudaSuccess)
+        return IF4_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
+}
+
+// Packed scales [row blocks][K steps][512 bytes] -> tensor map with a box of
+// one stage (4 K steps) x `blocks` row blocks.
+bool make_scales_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int blocks)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t steps = (cuuint64_t)((K + SK - 1) / SK) * KSTEPS;
+    const cuuint64_t dims[3] = {SF_STEP / 4, steps, (cuuint64_t)((rows + 127) / 128)};
+    const cuuint64_t strides[2] = {SF_STEP, steps * SF_STEP};
+    const cuuint32_t box[3] = {SF_STEP / 4, KSTEPS, (cuuint32_t)blocks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t packed_bytes(int64_t rows, int64_t K)
+{
+    return (size_t)((rows + 127) / 128) * (size_t)((K + SK - 1) / SK) * SF_BLOCK;
+}
+
+// The pair kernel takes problems above 128 rows and columns.
+bool use_pair(int64_t M, int64_t N) { return M > 128 && N > 128; }
+
+template <int VEC, int ODT>
+int launch_pair(const Problem &p, const Device &d)
+{
+    auto kernel = nvfp4_linear_pair<ODT>;
+    static std::once_flag once[MAX_DEVICES], occ_once[MAX_DEVICES];
+    static cudaError_t rcs[MAX_DEVICES];
+    static int resident[MAX_DEVICES];
+    const int rc = allow_smem(kernel, duo::SMEM, d, once, rcs);
+    if (rc != IF4_OK) return rc;
+    uint8_t *wa = static_cast<uint8_t *>(p.workspace), *wb = wa + packed_bytes(p.M, p.K);
+    CUtensorMap ma, mb, msa, msb;
+    if (!make_codes_map(&ma, p.a_codes, p.M, p.K, duo::PM) ||
+        !make_codes_map(&mb, p.b_codes, p.N, p.K, duo::BN / 2) ||
+        !make_scales_map(&msa, wa, p.M, p.K, 1) || !make_scales_map(&msb, wb, p.N, p.K, 2))
+        return IF4_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = p.st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int64_t warps = ((p.M + 127) / 128 + (p.N + 127) / 128) * ((p.K + UNIT - 1) / UNIT) * 2;
+    const int64_t blocks = (warps + 7) / 8, most = (int64_t)d.sms * 8;
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    const ScalePack sa{p.a_scales, wa, (int)p.M}, sb{p.b_scales, wb, (int)p.N};
+    if (cudaLaunchKernelEx(&cfg, pack_scales<VEC>, sa, sb, (int)p.K, p.err) != cudaSuccess)
+        return IF4_ERR_CUDA;
+
+    cfg.gridDim = dim3((unsigned)(2 * (d.sms / 2)), 1, 1);
+    cfg.blockDim = dim3(duo::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = duo::SMEM;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    // persistent: as many pairs as can be resident at once (the SMs of a pair
+    // share a GPC, so this can be below sms / 2)
+    std::call_once(occ_once[d.id], [&] {
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
+            resident[d.id] = n;
+        else
+            (void)cudaGetLastError();
+    });
+    const int64_t tiles = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + duo::BN - 1) / duo::BN);
+    int64_t pairs = resident[d.id] > 0 ? resident[d.id] : d.sms / 2;
+    if (pairs > d.sms / 2) pairs = d.sms / 2;
+    if (tiles < pairs) pairs = tiles;
+    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, p.a_ts, p.b_ts, p.c, (int)p.M, (int)p.N,
+                           (int)p.K, p.err) != cudaSuccess)
+        return IF4_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
+}
+
+template <int VEC, int ODT>
+int launch_linear(const Problem &p, const Device &d)
+{
+    if (use_pair(p.M, p.N)) return launch_pair<VEC, ODT>(p, d);
+    const int64_t units = (p.K + UNIT - 1) / UNIT;
+    auto ranks_for = [&](int64_t tiles) {
+        int s = 1;
+        while (s < 8 && 2 * s <= units && tiles * s < d.sms * 3 / 4) s *= 2;
+        return s;
+    };
+    const int64_t wt = (p.N + split::WR - 1) / split::WR;
+    if (p.M <= 16) return launch_split<16, VEC, ODT>(p, d, ranks_for(wt));
+    if (p.M <= 32) return launch_split<32, VEC, ODT>(p, d, ranks_for(wt));
+    if (p.M <= 64) return launch_split<64, VEC, ODT>(p, d, ranks_for(wt));
+    return launch_split<128, VEC, ODT>(p, d, ranks_for(wt * ((p.M + 127) / 128)));
+}
+
+}  // namespace
+
+extern "C" size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > MAX_MN || N > MAX_MN || K > MAX_K) return 0;
+    return use_pair(M, N) ? packed_bytes(M, K) + packed_bytes(N, K) : 0;
+}
+
+extern "C" int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, const float *a_ts,
+                            const uint8_t *b_codes, const uint8_t *b_scales, const float *b_ts,
+                            int64_t M, int64_t N, int64_t K, void *workspace, size_t ws_bytes,
+                            void *c, int c_dtype, int *err_flag, void *stream)
+{
+    if (M < 0 || N < 0 || K < 32 || K % 32 != 0) return IF4_ERR_SHAPE;
+    if (M > MAX_MN || N > MAX_MN || K > MAX_K) return IF4_ERR_SHAPE;
+    if (c_dtype != IF4_F32 && c_dtype != IF4_BF16 && c_dtype != IF4_F16) return IF4_ERR_DTYPE;
+    if (!err_flag) return IF4_ERR_NULL;
+    if (M == 0 || N == 0) return IF4_OK;
+    if (!a_codes || !a_scales || !a_ts || !b_codes || !b_scales || !b_ts || !c) return IF4_ERR_NULL;
+    auto misaligned = [](const void *q, uintptr_t n) { return reinterpret_cast<uintptr_t>(q) % n != 0; };
+    if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 4) ||
+        misaligned(b_scales, 4) || misaligned(a_ts, 4) || misaligned(b_ts, 4) ||
+        misaligned(err_flag, 4) || misaligned(c, c_dtype == IF4_F32 ? 4 : 2))
+        return IF4_ERR_ALIGN;
+    const size_t need = nvfp4_linear_workspace_bytes(M, N, K);
+    if (need && (!workspace || ws_bytes < need)) return IF4_ERR_WORKSPACE;
+    if (need && misaligned(workspace, 256)) return IF4_ERR_ALIGN;
+    Device d;
+    const int rc = current_device(d);
+    if (rc != IF4_OK) return rc;
+    const Problem p{a_codes, a_scales, b_codes, b_scales, a_ts, b_ts, M, N, K, workspace, c, err_flag,
+                    static_cast<cudaStream_t>(stream)};
+    const int vec = K % 256 == 0 && !misaligned(a_scales, 16) && !misaligned(b_scales, 16) ? 16
+                    : K % 64 == 0 ? 4 : 2;
+    auto typed = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        return c_dtype == IF4_F32    ? launch_linear<V, IF4_F32>(p, d)
+               : c_dtype == IF4_BF16 ? launch_linear<V, IF4_BF16>(p, d)
+                                     : launch_linear<V, IF4_F16>(p, d);
+    };
+    return vec == 16  ? typed(std::integral_constant<int, 16>{})
+           : vec == 4 ? typed(std::integral_constant<int, 4>{})
+                      : typed(std::integral_constant<int, 2>{});
+}

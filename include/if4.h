@@ -357,6 +357,33 @@ int if4_linear_quantized(const uint8_t *a_codes, const uint8_t *a_scales, const 
                          int *err_flag, void *stream);
 
 /*
+ * NVFP4 x NVFP4 linear on the block-scaled tensor cores: C[M, N] = c_dtype_RNE(
+ * fl(a_ts * b_ts) * sum_k A[m, k] B[n, k]) (C = A B^T), where A (activations, [M, K]) and B
+ * (weights, [N, K]) are NVFP4 along K as nvfp4_quantize, nvfp4_4over6_quantize
+ * or nvfp4_quantize_t write them: A[m, k] = q * E4M3(scale), the tensor scale
+ * left out.  The codes go to tcgen05.mma (kind::mxf4nvf4, one UE4M3 scale per
+ * 16 elements) undecoded; the sum is kept in binary32.  IF4 tensors with INT4
+ * groups (bit 7 of a scale byte set) are not NVFP4: such a byte sets
+ * IF4_DEV_BAD_SCALE and C is unspecified (use if4_linear).  A NaN scale byte
+ * (0x7F) makes every element that reads it NaN.
+ *
+ * c_dtype: IF4_BF16, IF4_F16 or IF4_F32; C dense.  M, N >= 0 (nothing to do at
+ * 0), K >= 32, K % 32 == 0 (a row of codes is a whole number of 16-byte
+ * units), M and N at most 2^22, K at most 2^20.  a_codes, b_codes 16-byte
+ * aligned, a_scales, b_scales 4-byte, C aligned to its element.  workspace
+ * (256-byte aligned, nvfp4_linear_workspace_bytes; 0 and NULL for few rows or
+ * columns) holds both operands' scales in the tensor cores' order during the
+ * call; calls that may run at the same time need one each.  err_flag must not
+ * be NULL (IF4_DEV_BAD_SCALE, IF4_DEV_TIMEOUT).  The pages compare IF4 with NVFP4
+ * throughout (gist.science section 4) and name no kernel for it.
+ */
+size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, const float *a_ts,
+                 const uint8_t *b_codes, const uint8_t *b_scales, const float *b_ts,
+                 int64_t M, int64_t N, int64_t K, void *workspace, size_t ws_bytes,
+                 void *c, int c_dtype, int *err_flag, void *stream);
+
+/*
  * IF6 and IF3: the same adaptive FP/INT choice at 6 and 3 bits per value.
  * The pages name both formats and say the adaptive choice carries over to
  * other bit widths ("Adaptive Block-Scaled Data Types", abstract; companion
