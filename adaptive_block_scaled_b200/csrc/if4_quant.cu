@@ -39,44 +39,13 @@
 #include "if4_device.cuh"
 #include "if4_decode.cuh"
 #include "if4_encode.cuh"
+#include "if4_host.cuh"
 #include "if4_internal.h"
+#include "if4_load.cuh"
 
 using namespace if4dev;
 
 namespace {
-
-// --------------------------------------------------------- group loads ----
-
-// Raw bits of one group: 16-bit types fill w[0..7], f32 fills w[0..15].
-template <int DT>
-struct Raw {
-    uint32_t w[DT == DT_F32 ? 16 : 8];
-};
-
-template <int DT, bool V8>
-__device__ __forceinline__ void load_group(const char *p, Raw<DT> &r)
-{
-    if constexpr (DT == DT_F32) {
-        if constexpr (V8) {
-            uint32_t a[8], b[8];
-            ld_nc_v8(p, a);
-            ld_nc_v8(p + 32, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) { r.w[i] = a[i]; r.w[8 + i] = b[i]; }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                ld_nc_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
-        }
-    } else {
-        if constexpr (V8) {
-            ld_nc_v8(p, r.w);
-        } else {
-            ld_nc_v4(p, r.w[0], r.w[1], r.w[2], r.w[3]);
-            ld_nc_v4(p + 16, r.w[4], r.w[5], r.w[6], r.w[7]);
-        }
-    }
-}
 
 // The same loads with an L2 cache policy.
 template <int DT, bool V8>
@@ -101,49 +70,6 @@ __device__ __forceinline__ void load_group_pol(const char *p, Raw<DT> &r, uint64
         } else {
             ld_nc_v4_pol(p, r.w[0], r.w[1], r.w[2], r.w[3], pol);
             ld_nc_v4_pol(p + 16, r.w[4], r.w[5], r.w[6], r.w[7], pol);
-        }
-    }
-}
-
-// Unpack to 8 float pairs (element 2j low, 2j+1 high) and the group's max |x|
-// as float bits; *nonfinite is set for Inf/NaN.
-template <int DT>
-__device__ __forceinline__ float unpack_group(const Raw<DT> &r, f2_t (&x)[8], bool &nonfinite)
-{
-    if constexpr (DT == DT_F32) {
-        // max |x| in two chains of one instruction per element (NaN
-        // propagates; the sign bit it leaves is masked off)
-        uint32_t m0 = 0, m1 = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t a = r.w[2 * j], b = r.w[2 * j + 1];
-            m0 = absmax_f32(m0, __uint_as_float(a));
-            m1 = absmax_f32(m1, __uint_as_float(b));
-            x[j] = f2_pack(__uint_as_float(a), __uint_as_float(b));
-        }
-        const uint32_t m = absmax_f32(m0, __uint_as_float(m1)) & 0x7FFFFFFFu;
-        nonfinite = m >= 0x7F800000u;
-        return __uint_as_float(m);
-    } else {
-        // max(|a|, |b|) per 16-bit lane in one instruction (the sign bit it
-        // leaves is ignored); NaN propagates, so Inf/NaN show up in the max
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t w = r.w[j];
-            m = (DT == DT_BF16) ? absmax_bf16x2(m, w) : absmax_f16x2(m, w);
-            if constexpr (DT == DT_BF16)
-                x[j] = f2_from_bf16x2(w);
-            else
-                x[j] = f2_pack(f16lo_to_f32(w), f16hi_to_f32(w));
-        }
-        const uint32_t m16 = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
-        if constexpr (DT == DT_BF16) {
-            nonfinite = m16 >= 0x7F80u;
-            return __uint_as_float(m16 << 16);
-        } else {
-            nonfinite = m16 >= 0x7C00u;
-            return f16lo_to_f32(m16);
         }
     }
 }
@@ -273,14 +199,6 @@ __device__ __forceinline__ void reload_group(const char *p, uint32_t signs, floa
     }
     if constexpr (RHT) hadamard16_scalar(y, signs);
 }
-
-__device__ __forceinline__ bool ts_valid(float ts)
-{
-    return ts >= kTsFloor && ts <= kTsCeil;   // false for NaN
-}
-
-template <int DT>
-__host__ __device__ constexpr int elem_bytes() { return DT == DT_F32 ? 4 : 2; }
 
 __device__ __forceinline__ const char *group_ptr(const char *x, uint32_t g, bool contig,
                                                  uint32_t gpr, int64_t ld_bytes, int gbytes)
@@ -1043,39 +961,6 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
 
 // ------------------------------------------------------------ host side ----
 
-struct DeviceInfo {
-    int sm_count = 0;
-    int cc_major = 0;
-};
-
-bool device_info(DeviceInfo &out)
-{
-    static std::mutex mu;
-    static DeviceInfo cache[64];
-    static bool have[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!have[dev]) {
-        DeviceInfo d;
-        if (cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return false;
-        if (cudaDeviceGetAttribute(&d.cc_major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-            return false;
-        cache[dev] = d;
-        have[dev] = true;
-    }
-    out = cache[dev];
-    return true;
-}
-
-int check_device(DeviceInfo &d)
-{
-    if (!device_info(d)) return IF4_ERR_CUDA;
-    if (d.cc_major != 10) return IF4_ERR_DEVICE;
-    return IF4_OK;
-}
-
 template <typename K>
 int resident_blocks(K kernel, int threads)
 {
@@ -1083,66 +968,6 @@ int resident_blocks(K kernel, int threads)
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)
         n = 1;
     return n;
-}
-
-int elem_size(int dt)
-{
-    switch (dt) {
-    case IF4_F32: return 4;
-    case IF4_BF16: return 2;
-    case IF4_F16: return 2;
-    default: return 0;
-    }
-}
-
-struct Shape {
-    uint32_t gpr = 0, ngroups = 0;
-    int64_t ld_bytes = 0;
-    bool contig = false, v8 = false;
-};
-
-// Validate a dense input or output tensor description.
-int check_tensor(const void *p, int dt, int64_t rows, int64_t cols, int64_t ld, Shape &s)
-{
-    const int es = elem_size(dt);
-    if (es == 0) return IF4_ERR_DTYPE;
-    if (rows < 0 || cols < 0 || cols % 16 != 0 || ld < cols) return IF4_ERR_SHAPE;
-    if (rows > 0 && (cols / 16) > 0 && rows > (int64_t)0x7FFFFFFF / (cols / 16)) return IF4_ERR_SHAPE;
-    if (rows > 0 && cols > 0 && p == nullptr) return IF4_ERR_NULL;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    if (a % 16 != 0 || (ld * es) % 16 != 0) return IF4_ERR_ALIGN;
-    s.gpr = (uint32_t)(cols / 16);
-    s.ngroups = (uint32_t)(rows * (cols / 16));
-    s.ld_bytes = ld * es;
-    s.contig = (ld == cols) || rows <= 1;
-    s.v8 = (a % 32 == 0) && (s.ld_bytes % 32 == 0);
-    return IF4_OK;
-}
-
-int launch_status()
-{
-    return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
-}
-
-// Launch of the stream-ordered kernels (amax, scale, quantize, dequantize)
-// with programmatic dependent launch: each such kernel lets the next one be
-// scheduled while it drains, and waits for its predecessor's results before
-// reading anything (pdl_enter), so stream order holds as usual.
-template <typename... KArgs, typename... Args>
-int launch_k(void (*k)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(block, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k, args...) != cudaSuccess) return IF4_ERR_CUDA;
-    return launch_status();
 }
 
 // Blocks to launch: enough for every work item, capped at one full wave of

@@ -28,6 +28,7 @@
 
 #include "../../include/if4.h"
 #include "if4_device.cuh"
+#include "if4_host.cuh"
 #include "if4_tc.cuh"
 
 namespace {
@@ -781,24 +782,7 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
 
 // ------------------------------------------------------------ host side ----
 
-constexpr int MAX_DEVICES = 64;
 constexpr int64_t MAX_MN = 1 << 22, MAX_K = 1 << 20;
-
-// What a launch needs to know of the current device, read once per device.
-struct Device {
-    int id, sms;
-};
-
-int current_device(Device &d)
-{
-    static std::once_flag once[MAX_DEVICES];
-    static int sms[MAX_DEVICES], rcs[MAX_DEVICES];
-    if (cudaGetDevice(&d.id) != cudaSuccess || d.id < 0 || d.id >= MAX_DEVICES) return IF4_ERR_CUDA;
-    const int id = d.id;
-    std::call_once(once[id], [id] { rcs[id] = sm_count_checked(sms[id]); });
-    d.sms = sms[id];
-    return rcs[id];
-}
 
 // Codes [rows, K / 2] -> tensor map with a (128 bytes x box_rows) box.
 bool make_codes_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box_rows)
@@ -826,7 +810,7 @@ struct Problem {
 
 // The kernel's shared-memory limit is raised once per device and kernel.
 template <typename Kernel>
-int allow_smem(Kernel kernel, int bytes, const Device &d, std::once_flag (&once)[MAX_DEVICES],
+int allow_smem(Kernel kernel, int bytes, const DeviceInfo &d, std::once_flag (&once)[MAX_DEVICES],
                cudaError_t (&rcs)[MAX_DEVICES])
 {
     std::call_once(once[d.id], [&] {
@@ -836,7 +820,7 @@ int allow_smem(Kernel kernel, int bytes, const Device &d, std::once_flag (&once)
 }
 
 template <int NT, int VEC, int ODT>
-int launch_split(const Problem &p, const Device &d, int ranks)
+int launch_split(const Problem &p, const DeviceInfo &d, int ranks)
 {
     using C = split::Cfg<NT>;
     auto kernel = nvfp4_linear_split<NT, VEC, ODT>;
@@ -894,7 +878,7 @@ size_t packed_bytes(int64_t rows, int64_t K)
 bool use_pair(int64_t M, int64_t N) { return M > 128 && N > 128; }
 
 template <int VEC, int ODT>
-int launch_pair(const Problem &p, const Device &d)
+int launch_pair(const Problem &p, const DeviceInfo &d)
 {
     auto kernel = nvfp4_linear_pair<ODT>;
     static std::once_flag once[MAX_DEVICES], occ_once[MAX_DEVICES];
@@ -916,14 +900,14 @@ int launch_pair(const Problem &p, const Device &d)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int64_t warps = ((p.M + 127) / 128 + (p.N + 127) / 128) * ((p.K + UNIT - 1) / UNIT) * 2;
-    const int64_t blocks = (warps + 7) / 8, most = (int64_t)d.sms * 8;
+    const int64_t blocks = (warps + 7) / 8, most = (int64_t)d.sm_count * 8;
     cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     const ScalePack sa{p.a_scales, wa, (int)p.M}, sb{p.b_scales, wb, (int)p.N};
     if (cudaLaunchKernelEx(&cfg, pack_scales<VEC>, sa, sb, (int)p.K, p.err) != cudaSuccess)
         return IF4_ERR_CUDA;
 
-    cfg.gridDim = dim3((unsigned)(2 * (d.sms / 2)), 1, 1);
+    cfg.gridDim = dim3((unsigned)(2 * (d.sm_count / 2)), 1, 1);
     cfg.blockDim = dim3(duo::THREADS, 1, 1);
     cfg.dynamicSmemBytes = duo::SMEM;
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -941,8 +925,8 @@ int launch_pair(const Problem &p, const Device &d)
             (void)cudaGetLastError();
     });
     const int64_t tiles = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + duo::BN - 1) / duo::BN);
-    int64_t pairs = resident[d.id] > 0 ? resident[d.id] : d.sms / 2;
-    if (pairs > d.sms / 2) pairs = d.sms / 2;
+    int64_t pairs = resident[d.id] > 0 ? resident[d.id] : d.sm_count / 2;
+    if (pairs > d.sm_count / 2) pairs = d.sm_count / 2;
     if (tiles < pairs) pairs = tiles;
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
     if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, p.a_ts, p.b_ts, p.c, (int)p.M, (int)p.N,
@@ -952,13 +936,13 @@ int launch_pair(const Problem &p, const Device &d)
 }
 
 template <int VEC, int ODT>
-int launch_linear(const Problem &p, const Device &d)
+int launch_linear(const Problem &p, const DeviceInfo &d)
 {
     if (use_pair(p.M, p.N)) return launch_pair<VEC, ODT>(p, d);
     const int64_t units = (p.K + UNIT - 1) / UNIT;
     auto ranks_for = [&](int64_t tiles) {
         int s = 1;
-        while (s < 8 && 2 * s <= units && tiles * s < d.sms * 3 / 4) s *= 2;
+        while (s < 8 && 2 * s <= units && tiles * s < d.sm_count * 3 / 4) s *= 2;
         return s;
     };
     const int64_t wt = (p.N + split::WR - 1) / split::WR;
@@ -995,8 +979,8 @@ extern "C" int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, con
     const size_t need = nvfp4_linear_workspace_bytes(M, N, K);
     if (need && (!workspace || ws_bytes < need)) return IF4_ERR_WORKSPACE;
     if (need && misaligned(workspace, 256)) return IF4_ERR_ALIGN;
-    Device d;
-    const int rc = current_device(d);
+    DeviceInfo d;
+    const int rc = check_device(d);
     if (rc != IF4_OK) return rc;
     const Problem p{a_codes, a_scales, b_codes, b_scales, a_ts, b_ts, M, N, K, workspace, c, err_flag,
                     static_cast<cudaStream_t>(stream)};
