@@ -73,6 +73,16 @@ def _load():
         "if4_linear_fused": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp],
         "if4_linear_quantized": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
                                  ctypes.c_size_t, _vp, _vp, _vp, _vp, _vp, _vp],
+        "if4_quantize_t": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp],
+        "nvfp4_quantize_t": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _int, _vp,
+                             _vp],
+        "if4_rms_norm_quantize": [_vp, _i64, _vp, _i64, _vp, _int, _int, _i64, _i64,
+                                  ctypes.c_float, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+        "nvfp4_rms_norm_quantize": [_vp, _i64, _vp, _i64, _vp, _int, _int, _i64, _i64,
+                                    ctypes.c_float, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+        "if4_rms_norm_backward_workspace_bytes": [_i64, _i64],
+        "if4_rms_norm_backward": [_vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _i64,
+                                  _i64, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp],
         "nvfp4_linear_workspace_bytes": [_i64, _i64, _i64],
         "nvfp4_linear": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_size_t,
                          _vp, _int, _vp, _vp],
@@ -92,8 +102,9 @@ def _load():
     lib.if4_status_str.restype = ctypes.c_char_p
     if hasattr(lib, "if4_linear_workspace_bytes"):
         lib.if4_linear_workspace_bytes.restype = ctypes.c_size_t
-    if hasattr(lib, "nvfp4_linear_workspace_bytes"):
-        lib.nvfp4_linear_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("nvfp4_linear_workspace_bytes", "if4_rms_norm_backward_workspace_bytes"):
+        if hasattr(lib, name):
+            getattr(lib, name).restype = ctypes.c_size_t
     return lib
 
 
@@ -411,6 +422,185 @@ def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     nvfp4_linear(*a, *b, ws, c, err_flag, stream)
     return c
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """A 2-D tensor whose rows are contiguous and do not overlap: its row
+    stride in elements."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be 2-D" + ("" if shape is None else f" of {tuple(shape)}"))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0) if rows > 1 and cols > 0 else cols
+
+
+def _entry(mode, name):
+    if mode not in ("if4", "nvfp4"):
+        raise ValueError(f'{name}: mode must be "if4" or "nvfp4"')
+    return f"{mode}_{name}"
+
+
+def _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream):
+    dev = _device(entry, x, codes, scales, codes_t, scales_t, ts, err_flag)
+    ld = _rows(x, "x")
+    rows, cols = x.shape
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    if codes is not None:
+        _u8(codes, "codes", (rows, cols // 2))
+        _u8(scales, "scales", (rows, cols // 16))
+    _u8(codes_t, "codes_t", (cols, rows // 2))
+    _u8(scales_t, "scales_t", (cols, rows // 16))
+    _word(ts, "ts", torch.float32)
+    _word(err_flag, "err_flag", torch.int32)
+    with torch.cuda.device(dev):
+        _check(getattr(lib, entry)(_ptr(x), _dtype(x, "x"), rows, cols, ld, _ptr(codes),
+                                   _ptr(scales), _ptr(codes_t), _ptr(scales_t), _ptr(ts),
+                                   int(ts_mode), _ptr(err_flag), _stream(stream)), entry)
+
+
+def if4_quantize_t(x, codes, scales, codes_t, scales_t, ts, ts_mode=TS_COMPUTE, err_flag=None,
+                   stream=None):
+    """IF4 of x^T (codes_t [cols, rows/2], scales_t [cols, rows/16]) and, when
+    codes and scales are given, of x as well."""
+    _quantize_t_call("if4_quantize_t", x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag,
+                     stream)
+
+
+def nvfp4_quantize_t(x, codes, scales, codes_t, scales_t, ts, ts_mode=TS_COMPUTE, err_flag=None,
+                     stream=None):
+    """NVFP4 of x^T and, when codes and scales are given, of x as well."""
+    _quantize_t_call("nvfp4_quantize_t", x, codes, scales, codes_t, scales_t, ts, ts_mode,
+                     err_flag, stream)
+
+
+def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=None):
+    """Quantize a 2-D tensor along its rows with mode "if4" or "nvfp4".
+    Returns (codes_t, scales_t, ts) of x^T or, with_rows, (codes, scales,
+    codes_t, scales_t, ts) of x and of x^T under one tensor scale.  ts=None
+    computes it; a float32 tensor is used as given."""
+    entry = _entry(mode, "quantize_t")
+    _rows(x, "x")
+    (rows, cols), dev = x.shape, x.device
+    u8 = dict(dtype=torch.uint8, device=dev)
+    codes_t, scales_t = torch.empty((cols, rows // 2), **u8), torch.empty((cols, rows // 16), **u8)
+    codes = torch.empty((rows, cols // 2), **u8) if with_rows else None
+    scales = torch.empty((rows, cols // 16), **u8) if with_rows else None
+    if ts is None:
+        ts_t, ts_mode = torch.empty(1, dtype=torch.float32, device=dev), TS_COMPUTE
+    else:
+        ts_t, ts_mode = ts, TS_GIVEN
+    _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts_t, ts_mode, err_flag, stream)
+    if with_rows:
+        return codes, scales, codes_t, scales_t, ts_t
+    return codes_t, scales_t, ts_t
+
+
+def _norm_weight(weight, cols, dtype):
+    if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous tensor of {cols} elements")
+    if weight.dtype not in (dtype, torch.float32):
+        raise ValueError(f"weight must be {dtype} or float32")
+
+
+def _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
+                   stream):
+    dev = _device(entry, x, residual, weight, h, rstd, codes, scales, ts, amax, err_flag)
+    ld = _rows(x, "x")
+    rows, cols = x.shape
+    ld_res = 0 if residual is None else _rows(residual, "residual", x.dtype, x.shape)
+    ld_h = 0 if h is None else _rows(h, "h", x.dtype, x.shape)
+    _norm_weight(weight, cols, x.dtype)
+    _u8(codes, "codes", (rows, cols // 2))
+    _u8(scales, "scales", (rows, cols // 16))
+    if rstd is not None and (rstd.dtype != torch.float32 or tuple(rstd.shape) != (rows,)
+                             or not rstd.is_contiguous()):
+        raise ValueError(f"rstd must be a contiguous float32 tensor of {rows} elements")
+    _word(ts, "ts", torch.float32)
+    _word(amax, "amax", torch.float32)
+    _word(err_flag, "err_flag", torch.int32)
+    with torch.cuda.device(dev):
+        _check(getattr(lib, entry)(_ptr(x), ld, _ptr(residual), ld_res, _ptr(weight),
+                                   _dtype(weight, "weight"), _dtype(x, "x"), rows, cols,
+                                   float(eps), _ptr(h), ld_h, _ptr(rstd), _ptr(codes),
+                                   _ptr(scales), _ptr(ts), _ptr(amax), _ptr(err_flag),
+                                   _stream(stream)), entry)
+
+
+def if4_rms_norm_quantize(x, residual, weight, eps, h, rstd, codes, scales, ts, amax=None,
+                          err_flag=None, stream=None):
+    """RMS norm of x (+ residual) quantized to IF4 under the given ts; residual,
+    h, rstd and amax may be None."""
+    _rms_norm_call("if4_rms_norm_quantize", x, residual, weight, eps, h, rstd, codes, scales, ts,
+                   amax, err_flag, stream)
+
+
+def nvfp4_rms_norm_quantize(x, residual, weight, eps, h, rstd, codes, scales, ts, amax=None,
+                            err_flag=None, stream=None):
+    """RMS norm of x (+ residual) quantized to NVFP4 under the given ts."""
+    _rms_norm_call("nvfp4_rms_norm_quantize", x, residual, weight, eps, h, rstd, codes, scales, ts,
+                   amax, err_flag, stream)
+
+
+def rms_norm_quantize(x, weight, ts, residual=None, eps=1e-6, mode="if4", amax=None,
+                      err_flag=None, stream=None):
+    """RMS norm of x (+ residual), quantized with mode "if4" or "nvfp4" under
+    the float32 tensor ts.  Returns (codes, scales, h, rstd): h = x + residual
+    (x itself without a residual) and rstd [rows] are what rms_norm_backward
+    takes.  amax: a float32 tensor raised to max |y|, for the next ts."""
+    entry = _entry(mode, "rms_norm_quantize")
+    _rows(x, "x")
+    (rows, cols), dev = x.shape, x.device
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    h = None if residual is None else torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
+                   stream)
+    return codes, scales, x if h is None else h, rstd
+
+
+def if4_rms_norm_backward_workspace_bytes(rows, cols):
+    return int(lib.if4_rms_norm_backward_workspace_bytes(int(rows), int(cols)))
+
+
+def if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, workspace, stream=None):
+    """Gradient of the norm into dx (x's type) and dweight (float32 [cols])."""
+    name = "if4_rms_norm_backward"
+    dev = _device(name, dy, h, weight, rstd, dres, dx, dweight, workspace)
+    rows, cols = h.shape if h.dim() == 2 else (0, 0)
+    ld_h = _rows(h, "h")
+    ld_dy = _rows(dy, "dy", h.dtype, h.shape)
+    ld_dx = _rows(dx, "dx", h.dtype, h.shape)
+    ld_dres = 0 if dres is None else _rows(dres, "dres", h.dtype, h.shape)
+    _norm_weight(weight, cols, h.dtype)
+    for t, n, k in ((rstd, "rstd", rows), (dweight, "dweight", cols)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (k,) or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous float32 tensor of {k} elements")
+    with torch.cuda.device(dev):
+        _check(lib.if4_rms_norm_backward(_ptr(dy), ld_dy, _ptr(h), ld_h, _ptr(weight),
+                                         _dtype(weight, "weight"), _ptr(rstd), _ptr(dres), ld_dres,
+                                         _dtype(h, "h"), rows, cols, _ptr(dx), ld_dx,
+                                         _ptr(dweight), _ptr(workspace),
+                                         0 if workspace is None else
+                                         workspace.numel() * workspace.element_size(),
+                                         _stream(stream)), name)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dres=None, stream=None):
+    """Gradient of rms_norm_quantize (straight through the quantizer) from dy,
+    the gradient of the norm's output, and dres, that of h past the norm.
+    Returns (dx, dweight): dx for x and the residual alike, dweight float32."""
+    rows, cols = h.shape
+    dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
+    dweight = torch.empty(cols, dtype=torch.float32, device=h.device)
+    need = if4_rms_norm_backward_workspace_bytes(rows, cols)
+    ws = torch.empty(need, dtype=torch.uint8, device=h.device) if need else None
+    if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, ws, stream)
+    return dx, dweight
 
 
 # ------------------------------------------------------- IF6 and IF3 ---

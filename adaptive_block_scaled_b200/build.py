@@ -27,11 +27,13 @@ SOURCES = [
     ("if4_quant.cu", ["-fmad=false"]),
     ("if4_linear.cu", ["-fmad=false"]),   # shares the IF4 encoder (no contraction)
     ("if4_linear_noalloc.cu", []),
+    ("if4_quant_t.cu", ["-fmad=false"]),
+    ("if4_norm.cu", ["-fmad=false"]),     # h and y take the contract's roundings
     ("nvfp4_linear.cu", ["-fmad=false"]),
     ("ifw_quant.cu", ["-fmad=false"]),    # IF6 / IF3: the same arithmetic contract
 ]
 HEADERS = ["if4_device.cuh", "if4_encode.cuh", "if4_decode.cuh", "if4_internal.h", "if4_tc.cuh",
-           "exports.map"]
+           "if4_load.cuh", "if4_host.cuh", "exports.map"]
 
 
 def _nvcc():

@@ -1,0 +1,447 @@
+// RMS norm with the residual's addition and a 4-bit output, and its gradient
+// (sm_100a).
+//
+// Forward, per row of x [R, C]:
+//   h    = RN(x + r)                     the residual stream, in x's type
+//   rstd = fl32(1 / sqrt(sum(h^2) / C + eps))    the sum and the root in binary64
+//   y    = fl(fl(h * rstd) * w)          binary32
+//   codes, scales = IF4 or NVFP4 of y under the given tensor scale
+// y never reaches memory.  The binary64 sum makes rstd the correctly rounded
+// value whatever the order of the additions, up to ties that a binary64 sum
+// cannot resolve: a row's codes then depend on nothing but the row, and equal
+// those of quantizing y computed any other way that takes the same roundings.
+// (A binary32 sum moves rstd by a few steps, and with it values next to a
+// rounding border of the 4-bit grid by a whole step.)
+//
+// Backward, with n = h * rstd the normalized row, g = dy * w:
+//   dx = RN(dres + rstd * (g - n * mean(g * n))),   dw = sum over rows of dy * n.
+// The quantizer passes gradients straight through.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/if4.h"
+#include "if4_device.cuh"
+#include "if4_encode.cuh"
+#include "if4_host.cuh"
+#include "if4_load.cuh"
+
+namespace {
+
+constexpr int NORM_THREADS = 256;
+
+// A group's 16 raw values as binary32 pairs.
+template <int DT>
+__device__ __forceinline__ void to_pairs(const Raw<DT> &r, f2_t (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (DT == DT_F32)
+            x[j] = f2_pack(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+        else if constexpr (DT == DT_BF16)
+            x[j] = f2_from_bf16x2(r.w[j]);
+        else
+            x[j] = f2_pack(f16lo_to_f32(r.w[j]), f16hi_to_f32(r.w[j]));
+    }
+}
+
+// Binary32 pairs rounded to the type's raw bits.
+template <int DT>
+__device__ __forceinline__ void to_raw(const f2_t (&x)[8], Raw<DT> &r)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float lo, hi;
+        f2_unpack(x[j], lo, hi);
+        if constexpr (DT == DT_F32) {
+            r.w[2 * j] = __float_as_uint(lo);
+            r.w[2 * j + 1] = __float_as_uint(hi);
+        } else {
+            r.w[j] = DT == DT_BF16 ? bf16x2_from_f32(lo, hi) : f16x2_from_f32(lo, hi);
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_group(char *p, const Raw<DT> &r)
+{
+#pragma unroll
+    for (int q = 0; q < (DT == DT_F32 ? 4 : 2); ++q)
+        st_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
+}
+
+// Plain (coherent) 16-byte loads: h may be x's or the residual's own memory,
+// so these inputs are not read through the read-only path.
+template <int DT>
+__device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r)
+{
+#pragma unroll
+    for (int q = 0; q < (DT == DT_F32 ? 4 : 2); ++q)
+        asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]),
+                       "=r"(r.w[4 * q + 3])
+                     : "l"(p + 16 * q));
+}
+
+// Sum over a block of NORM_THREADS; every thread gets it.
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T *buf)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();                       // buf may still be read
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    T s = buf[0];
+#pragma unroll
+    for (int i = 1; i < NORM_THREADS / 32; ++i) s += buf[i];
+    return s;
+}
+
+struct NormArgs {
+    const char *x, *res, *w;        // w: binary32 or x's type
+    char *h;
+    int64_t ld_x, ld_res, ld_h;     // bytes
+    uint8_t *codes, *scales;
+    const float *ts;
+    float *rstd;
+    unsigned int *amax;
+    int *err;
+    int64_t rows;
+    int gpr;                        // groups per row
+    float eps;
+};
+
+// h of one group: x, or RN(x + residual).
+template <int DT>
+__device__ __forceinline__ void load_h(const NormArgs &a, int64_t row, int g, Raw<DT> &h)
+{
+    constexpr int GB = 16 * elem_bytes<DT>();
+    load_group_rw<DT>(a.x + row * a.ld_x + (int64_t)g * GB, h);
+    if (a.res) {
+        Raw<DT> r;
+        load_group_rw<DT>(a.res + row * a.ld_res + (int64_t)g * GB, r);
+        f2_t u[8], v[8];
+        to_pairs<DT>(h, u);
+        to_pairs<DT>(r, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = f2_add(u[j], v[j]);
+        to_raw<DT>(u, h);
+    }
+}
+
+// Any number of columns: a block per row, h formed twice (the second time
+// mostly from L2).
+template <int DT, int WT, int MODE>
+__global__ void __launch_bounds__(NORM_THREADS)
+rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
+{
+    pdl_enter();
+    __shared__ float inv_tab[128];
+    __shared__ double sums[NORM_THREADS / 32];
+    const float ts = *a.ts;
+    const float rts = __frcp_rn(ts);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && a.err)
+        atomicOr(a.err, IF4_DEV_BAD_SCALE);
+    fill_inv_tab(inv_tab, ts);
+    constexpr int GB = 16 * elem_bytes<DT>();
+    bool nonfinite = false;
+    uint32_t top = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        double s = 0.0;
+        for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
+            Raw<DT> h;
+            f2_t v[8];
+            load_h<DT>(a, row, g, h);
+            to_pairs<DT>(h, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float lo, hi;
+                f2_unpack(v[j], lo, hi);
+                s = fma((double)lo, (double)lo, s);
+                s = fma((double)hi, (double)hi, s);
+            }
+        }
+        s = block_sum(s, sums);
+        const float rstd = (float)(1.0 / sqrt(s / (double)(a.gpr * 16.0) + (double)a.eps));
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+        const f2_t RS = f2_pack(rstd, rstd);
+        for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
+            Raw<DT> h;
+            Raw<WT> wr;
+            f2_t v[8], w[8];
+            load_h<DT>(a, row, g, h);
+            if (a.h) store_group<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h);
+            load_group<WT, false>(a.w + (int64_t)g * 16 * elem_bytes<WT>(), wr);
+            to_pairs<DT>(h, v);
+            to_pairs<WT>(wr, w);
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = f2_mul(f2_mul(v[j], RS), w[j]);
+                float lo, hi;
+                f2_unpack(v[j], lo, hi);
+                m = absmax_f32(m, lo);
+                m = absmax_f32(m, hi);
+            }
+            m &= 0x7FFFFFFFu;
+            nonfinite |= m >= 0x7F800000u;
+            top = max(top, m);
+            const GroupCode c = encode_registers<MODE>(v, __uint_as_float(m), ts, rts, inv_tab);
+            const int64_t gi = row * a.gpr + g;
+            st_v2(a.codes + gi * 8, c.c0, c.c1);
+            st_u8(a.scales + gi, c.scale);
+        }
+    }
+    if (a.amax) {
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if ((threadIdx.x & 31) == 0) atomicMax(a.amax, top);
+    }
+    if (nonfinite && a.err) atomicOr(a.err, IF4_DEV_NONFINITE);
+}
+
+// -------------------------------------------------------------- gradient ----
+
+constexpr int BACK_BLOCKS = 296;     // blocks that share the rows, and partial sums of dw
+
+struct BackArgs {
+    const char *dy, *h, *w, *dres;
+    char *dx;
+    int64_t ld_dy, ld_h, ld_dres, ld_dx;   // bytes
+    const float *rstd;
+    float *part;                    // [BACK_BLOCKS][cols]
+    int64_t rows;
+    int gpr;
+};
+
+// dx, any number of columns: a block per row, dy and h read twice.
+template <int DT, int WT>
+__global__ void __launch_bounds__(NORM_THREADS)
+rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
+{
+    pdl_enter();
+    __shared__ float sums[NORM_THREADS / 32];
+    constexpr int GB = 16 * elem_bytes<DT>();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float rstd = a.rstd[row];
+        float s = 0.0f;
+        for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
+            Raw<DT> hr, dr;
+            Raw<WT> wr;
+            f2_t h[8], d[8], w[8];
+            load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr);
+            load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr);
+            load_group<WT, false>(a.w + (int64_t)g * 16 * elem_bytes<WT>(), wr);
+            to_pairs<DT>(hr, h);
+            to_pairs<DT>(dr, d);
+            to_pairs<WT>(wr, w);
+            f2_t acc = f2_pack(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc = f2_fma(f2_mul(d[j], w[j]), h[j], acc);
+            float lo, hi;
+            f2_unpack(acc, lo, hi);
+            s += lo + hi;
+        }
+        s = block_sum(s, sums);
+        // mean(g * n) * rstd, n = h * rstd
+        const float k = s * rstd * rstd / (float)(a.gpr * 16);
+        const f2_t RS = f2_pack(rstd, rstd), NK = f2_pack(-k, -k);
+        for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
+            Raw<DT> hr, dr, er;
+            Raw<WT> wr;
+            f2_t h[8], d[8], w[8], e[8];
+            load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr);
+            load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr);
+            load_group<WT, false>(a.w + (int64_t)g * 16 * elem_bytes<WT>(), wr);
+            to_pairs<DT>(hr, h);
+            to_pairs<DT>(dr, d);
+            to_pairs<WT>(wr, w);
+            if (a.dres) {
+                load_group_rw<DT>(a.dres + row * a.ld_dres + (int64_t)g * GB, er);
+                to_pairs<DT>(er, e);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f2_t v = f2_mul(f2_fma(h[j], NK, f2_mul(d[j], w[j])), RS);
+                d[j] = a.dres ? f2_add(v, e[j]) : v;
+            }
+            Raw<DT> o;
+            to_raw<DT>(d, o);
+            store_group<DT>(a.dx + row * a.ld_dx + (int64_t)g * GB, o);
+        }
+    }
+}
+
+// Partial sums of dw: block (i, c) adds rows i, i + n, ... for 256 columns.
+template <int DT>
+__global__ void __launch_bounds__(256)
+rms_norm_dw_kernel(const __grid_constant__ BackArgs a)
+{
+    pdl_enter();
+    constexpr int ES = elem_bytes<DT>();
+    const int col = blockIdx.y * 256 + threadIdx.x;
+    if (col >= a.gpr * 16) return;
+    auto value = [&](const char *p) {
+        if constexpr (DT == DT_F32)
+            return *reinterpret_cast<const float *>(p);
+        else if constexpr (DT == DT_BF16)
+            return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short *>(p) << 16);
+        else
+            return __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short *>(p)));
+    };
+    float s = 0.0f;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x)
+        s = fmaf(value(a.dy + row * a.ld_dy + (int64_t)col * ES),
+                 value(a.h + row * a.ld_h + (int64_t)col * ES) * a.rstd[row], s);
+    a.part[(int64_t)blockIdx.x * a.gpr * 16 + col] = s;
+}
+
+// dw: the partial sums in order.
+__global__ void __launch_bounds__(256)
+rms_norm_dw_sum_kernel(const float *__restrict__ part, int n, int cols, float *__restrict__ dw)
+{
+    pdl_enter();
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col >= cols) return;
+    float s = 0.0f;
+    for (int i = 0; i < n; ++i) s += part[(int64_t)i * cols + col];
+    dw[col] = s;
+}
+
+// ------------------------------------------------------------ host side ----
+
+bool misaligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+int check_weight(const void *w, int w_dtype, int x_dtype)
+{
+    if (w_dtype != x_dtype && w_dtype != IF4_F32) return IF4_ERR_DTYPE;
+    return misaligned(w, 16) ? IF4_ERR_ALIGN : IF4_OK;
+}
+
+// f(std::integral_constant<DT>, std::integral_constant<WT>) for a pair of types
+template <typename F>
+int by_types(int x_dtype, int w_dtype, F f)
+{
+    using F32 = std::integral_constant<int, DT_F32>;
+    using BF = std::integral_constant<int, DT_BF16>;
+    using HF = std::integral_constant<int, DT_F16>;
+    if (x_dtype == IF4_F32) return f(F32{}, F32{});
+    if (x_dtype == IF4_BF16) return w_dtype == IF4_F32 ? f(BF{}, F32{}) : f(BF{}, BF{});
+    return w_dtype == IF4_F32 ? f(HF{}, F32{}) : f(HF{}, HF{});
+}
+
+template <int MODE>
+int rms_norm_quantize_entry(const void *x, int64_t ld_x, const void *res, int64_t ld_res,
+                            const void *w, int w_dtype, int x_dtype, int64_t rows, int64_t cols,
+                            float eps, void *h, int64_t ld_h, float *rstd, uint8_t *codes,
+                            uint8_t *scales, const float *ts, float *amax, int *err_flag,
+                            void *stream)
+{
+    Shape s, sr, sh;
+    int rc = check_tensor(x, x_dtype, rows, cols, ld_x, s);
+    if (rc != IF4_OK) return rc;
+    if (res && (rc = check_tensor(res, x_dtype, rows, cols, ld_res, sr)) != IF4_OK) return rc;
+    if (h && (rc = check_tensor(h, x_dtype, rows, cols, ld_h, sh)) != IF4_OK) return rc;
+    if ((rc = check_weight(w, w_dtype, x_dtype)) != IF4_OK) return rc;
+    if (!(eps > 0.0f && eps <= 3.402823466e38f)) return IF4_ERR_MODE;
+    if (!ts || (s.ngroups > 0 && (!w || !codes || !scales))) return IF4_ERR_NULL;
+    if (misaligned(codes, 16) || misaligned(ts, 4) || misaligned(rstd, 4) || misaligned(amax, 4) ||
+        misaligned(err_flag, 4))
+        return IF4_ERR_ALIGN;
+    DeviceInfo d;
+    rc = check_device(d);
+    if (rc != IF4_OK) return rc;
+    if (s.ngroups == 0) return IF4_OK;
+    const NormArgs a{static_cast<const char *>(x), static_cast<const char *>(res),
+                     static_cast<const char *>(w), static_cast<char *>(h), s.ld_bytes, sr.ld_bytes,
+                     sh.ld_bytes, codes, scales, ts, rstd, reinterpret_cast<unsigned int *>(amax),
+                     err_flag, rows, (int)(cols / 16), eps};
+    return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
+        auto k = rms_norm_quantize_kernel<decltype(dt)::value, decltype(wt)::value, MODE>;
+        const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8);
+        return launch_k(k, grid, NORM_THREADS, static_cast<cudaStream_t>(stream), a);
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+int if4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, int64_t ld_res,
+                          const void *weight, int w_dtype, int x_dtype, int64_t rows, int64_t cols,
+                          float eps, void *h, int64_t ld_h, float *rstd, uint8_t *codes,
+                          uint8_t *scales, const float *ts, float *amax, int *err_flag, void *stream)
+{
+    return rms_norm_quantize_entry<Q_IF4>(x, ld_x, residual, ld_res, weight, w_dtype, x_dtype, rows,
+                                          cols, eps, h, ld_h, rstd, codes, scales, ts, amax,
+                                          err_flag, stream);
+}
+
+int nvfp4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, int64_t ld_res,
+                            const void *weight, int w_dtype, int x_dtype, int64_t rows,
+                            int64_t cols, float eps, void *h, int64_t ld_h, float *rstd,
+                            uint8_t *codes, uint8_t *scales, const float *ts, float *amax,
+                            int *err_flag, void *stream)
+{
+    return rms_norm_quantize_entry<Q_NVFP4>(x, ld_x, residual, ld_res, weight, w_dtype, x_dtype,
+                                            rows, cols, eps, h, ld_h, rstd, codes, scales, ts, amax,
+                                            err_flag, stream);
+}
+
+size_t if4_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
+{
+    if (rows < 1 || cols < 16 || cols % 16 != 0 || rows > 0x7FFFFFFF / (cols / 16)) return 0;
+    return (size_t)std::min<int64_t>(rows, BACK_BLOCKS) * (size_t)cols * sizeof(float);
+}
+
+int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t ld_h,
+                          const void *weight, int w_dtype, const float *rstd, const void *dres,
+                          int64_t ld_dres, int x_dtype, int64_t rows, int64_t cols, void *dx,
+                          int64_t ld_dx, float *dweight, void *workspace, size_t ws_bytes,
+                          void *stream)
+{
+    Shape sy, sh, sr, sx;
+    int rc = check_tensor(dy, x_dtype, rows, cols, ld_dy, sy);
+    if (rc == IF4_OK) rc = check_tensor(h, x_dtype, rows, cols, ld_h, sh);
+    if (rc == IF4_OK) rc = check_tensor(dx, x_dtype, rows, cols, ld_dx, sx);
+    if (rc == IF4_OK && dres) rc = check_tensor(dres, x_dtype, rows, cols, ld_dres, sr);
+    if (rc == IF4_OK) rc = check_weight(weight, w_dtype, x_dtype);
+    if (rc != IF4_OK) return rc;
+    if (cols > 0 && !dweight) return IF4_ERR_NULL;
+    if (sy.ngroups > 0 && (!weight || !rstd)) return IF4_ERR_NULL;
+    if (misaligned(rstd, 4) || misaligned(dweight, 4)) return IF4_ERR_ALIGN;
+    const size_t need = if4_rms_norm_backward_workspace_bytes(rows, cols);
+    if (need && (!workspace || ws_bytes < need)) return IF4_ERR_WORKSPACE;
+    if (need && misaligned(workspace, 256)) return IF4_ERR_ALIGN;
+    DeviceInfo d;
+    rc = check_device(d);
+    if (rc != IF4_OK) return rc;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (sy.ngroups == 0) {                // no rows: dweight is an empty sum
+        if (cols > 0 && cudaMemsetAsync(dweight, 0, (size_t)cols * 4, st) != cudaSuccess)
+            return IF4_ERR_CUDA;
+        return IF4_OK;
+    }
+    const BackArgs a{static_cast<const char *>(dy), static_cast<const char *>(h),
+                     static_cast<const char *>(weight), static_cast<const char *>(dres),
+                     static_cast<char *>(dx), sy.ld_bytes, sh.ld_bytes, sr.ld_bytes, sx.ld_bytes,
+                     rstd, static_cast<float *>(workspace), rows, (int)(cols / 16)};
+    const int parts = (int)std::min<int64_t>(rows, BACK_BLOCKS);
+    return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
+        constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)parts, (unsigned)((cols + 255) / 256), 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.stream = st;
+        if (cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel<DT>, a) != cudaSuccess) return (int)IF4_ERR_CUDA;
+        int r = launch_k(rms_norm_dw_sum_kernel, (unsigned)((cols + 255) / 256), 256u, st,
+                         (const float *)workspace, parts, (int)cols, dweight);
+        if (r != IF4_OK) return r;
+        const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8);
+        return launch_k(rms_norm_dx_kernel<DT, WT>, grid, (unsigned)NORM_THREADS, st, a);
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,288 @@
+// Quantizers along the rows (sm_100a): groups of 16 consecutive rows of one
+// column of x [R, C], i.e. the quantization of x^T along its last axis, as
+// codes [C, R / 2] and scales [C, R / 16]; optionally also the quantization
+// of x along its own last axis, from the same read.
+//
+// Why: a linear's gradients contract over the axes its forward pass does not
+// group.  With Y = X W^T (X [M, K], W [N, K], both grouped along K),
+//   dX = dY W     contracts over N: dY grouped along N, W^T along N,
+//   dW = dY^T X   contracts over M: dY^T and X^T grouped along M,
+// so each of X, W and dY is needed both ways.
+//
+// A block takes a tile of 128 x 128.  Each thread loads whole row groups (16
+// values, 32 or 64 bytes), encodes them when the row form is wanted, and
+// leaves the raw values in shared memory.  Then a thread reads 16 rows of two
+// neighbouring columns (one conflict-free word per row), which are two whole
+// column groups in registers, and encodes them with the same group encoder.
+// The column codes are put back in order through shared memory, so that the
+// tile's 64 code bytes of a column leave as one run.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/if4.h"
+#include "if4_device.cuh"
+#include "if4_encode.cuh"
+#include "if4_host.cuh"
+#include "if4_load.cuh"
+
+namespace {
+
+constexpr int TILE = 128;                 // rows and columns of a block's tile
+constexpr int TG = TILE / 16;             // groups along one side
+constexpr int CODE_PITCH = TILE / 2 + 8;  // staged code bytes per column
+constexpr int THREADS_T = 256;
+
+template <int DT>
+__host__ __device__ constexpr int tile_bytes()
+{
+    return TILE * TILE * elem_bytes<DT>();
+}
+
+template <int DT>
+__host__ __device__ constexpr int smem_t_bytes()
+{
+    return tile_bytes<DT>() + TILE * CODE_PITCH + TILE * TG;
+}
+
+__device__ __forceinline__ void sts_v4(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    *static_cast<uint4 *>(p) = make_uint4(a, b, c, d);
+}
+
+template <int DT, int MODE, bool ROWS, bool V8>
+__global__ void __launch_bounds__(THREADS_T)
+quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, int64_t cols,
+                  uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                  uint8_t *__restrict__ codes_t, uint8_t *__restrict__ scales_t,
+                  const float *__restrict__ ts_ptr, int *err, int check_ts)
+{
+    pdl_enter();
+    constexpr int ES = elem_bytes<DT>();
+    constexpr int GB = 16 * ES;
+    constexpr int PITCH = TILE * ES;
+    extern __shared__ __align__(16) uint8_t smem_t[];
+    uint8_t *tile = smem_t;
+    uint8_t *code_out = smem_t + tile_bytes<DT>();
+    uint8_t *scale_out = code_out + TILE * CODE_PITCH;
+    __shared__ float inv_tab[128];
+
+    const float ts = *ts_ptr;
+    const float rts = __frcp_rn(ts);
+    if (check_ts && blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && err)
+        atomicOr(err, IF4_DEV_BAD_SCALE);
+    fill_inv_tab(inv_tab, ts);
+
+    const int64_t col_tiles = (cols + TILE - 1) / TILE;
+    const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)col_tiles) * TILE;
+    const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_tiles) * TILE;
+    bool nonfinite = false;
+
+    // row groups: thread t takes group t % 8 of rows t / 8, + 32, + 64, + 96
+    const int lg = threadIdx.x & (TG - 1), lr = threadIdx.x / TG;
+    Raw<DT> raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + lr + 32 * i, c = c0 + 16 * lg;
+        if (r < rows && c < cols) {
+            load_group<DT, V8>(x + r * ld_bytes + c * ES, raw[i]);
+        } else {
+#pragma unroll
+            for (uint32_t &w : raw[i].w) w = 0u;
+        }
+    }
+    __syncthreads();                        // inv_tab
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = lr + 32 * i;
+        uint8_t *d = tile + row * PITCH + lg * GB;
+        // 16-byte pieces in an order that keeps the eight lanes of a store
+        // phase on different banks
+        constexpr int PIECES = GB / 16;
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            const int k = ES == 2 ? (q ^ ((lg >> 2) & 1)) : ((q + (lg >> 1)) & 3);
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = raw[i].w[e];
+#pragma unroll
+                for (int z = 1; z < PIECES; ++z) v[e] = k == z ? raw[i].w[4 * z + e] : v[e];
+            }
+            sts_v4(d + 16 * k, v[0], v[1], v[2], v[3]);
+        }
+        if constexpr (ROWS) {
+            const int64_t r = r0 + row, c = c0 + 16 * lg;
+            if (r < rows && c < cols) {
+                f2_t xv[8];
+                bool bad;
+                const float amax = unpack_group<DT>(raw[i], xv, bad);
+                const GroupCode g = encode_registers<MODE>(xv, amax, ts, rts, inv_tab);
+                const int64_t gi = r * (cols / 16) + c / 16;
+                st_v2(codes + gi * 8, g.c0, g.c1);
+                st_u8(scales + gi, g.scale);
+            }
+        }
+    }
+    __syncthreads();
+
+    // column groups: warp w takes row group w, a lane two neighbouring
+    // columns of each half of the tile
+    const int rg = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        const int col = h * (TILE / 2) + 2 * lane;
+        const uint8_t *p = tile + rg * 16 * PITCH + col * ES;
+        Raw<DT> a, b;
+        if constexpr (DT == DT_F32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(p + i * PITCH);
+                a.w[i] = w.x;
+                b.w[i] = w.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = *reinterpret_cast<const uint32_t *>(p + 2 * i * PITCH);
+                const uint32_t v = *reinterpret_cast<const uint32_t *>(p + (2 * i + 1) * PITCH);
+                a.w[i] = if4dev::prmt(u, v, 0x5410u);
+                b.w[i] = if4dev::prmt(u, v, 0x7632u);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            f2_t xv[8];
+            bool bad;
+            const float amax = unpack_group<DT>(k ? b : a, xv, bad);
+            nonfinite |= bad;
+            const GroupCode g = encode_registers<MODE>(xv, amax, ts, rts, inv_tab);
+            *reinterpret_cast<uint2 *>(code_out + (col + k) * CODE_PITCH + rg * 8) =
+                make_uint2(g.c0, g.c1);
+            scale_out[(col + k) * TG + rg] = (uint8_t)g.scale;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TILE * TG / THREADS_T; ++i) {
+        const int k = threadIdx.x + i * THREADS_T;
+        const int col = k / TG, g = k & (TG - 1);
+        const int64_t c = c0 + col, rgrp = r0 / 16 + g;
+        if (c < cols && rgrp < rows / 16) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(code_out + col * CODE_PITCH + g * 8);
+            const int64_t gi = c * (rows / 16) + rgrp;
+            st_v2(codes_t + gi * 8, w.x, w.y);
+            st_u8(scales_t + gi, scale_out[col * TG + g]);
+        }
+    }
+    if (nonfinite && err) atomicOr(err, IF4_DEV_NONFINITE);
+}
+
+// ------------------------------------------------------------ host side ----
+
+struct OutT {
+    uint8_t *codes, *scales, *codes_t, *scales_t;
+};
+
+template <int DT, int MODE, bool ROWS, bool V8>
+int launch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t cols, const OutT &o,
+                      const float *ts, int *err, int check_ts, cudaStream_t st, const DeviceInfo &d)
+{
+    auto kernel = quantize_t_kernel<DT, MODE, ROWS, V8>;
+    constexpr int SMEM = smem_t_bytes<DT>();
+    static std::once_flag once[MAX_DEVICES];
+    static cudaError_t rcs[MAX_DEVICES];
+    std::call_once(once[d.id], [&] {
+        rcs[d.id] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    });
+    if (rcs[d.id] != cudaSuccess) return IF4_ERR_CUDA;
+    const int64_t tiles = ((rows + TILE - 1) / TILE) * ((cols + TILE - 1) / TILE);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles, 1, 1);
+    cfg.blockDim = dim3(THREADS_T, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<const char *>(x), s.ld_bytes, rows, cols,
+                           o.codes, o.scales, o.codes_t, o.scales_t, ts, err, check_ts) !=
+        cudaSuccess)
+        return IF4_ERR_CUDA;
+    return launch_status();
+}
+
+template <int DT, int MODE>
+int dispatch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t cols, const OutT &o,
+                        const float *ts, int *err, int check_ts, cudaStream_t st,
+                        const DeviceInfo &d)
+{
+    if (o.codes)
+        return s.v8 ? launch_quantize_t<DT, MODE, true, true>(s, x, rows, cols, o, ts, err, check_ts, st, d)
+                    : launch_quantize_t<DT, MODE, true, false>(s, x, rows, cols, o, ts, err, check_ts, st, d);
+    return s.v8 ? launch_quantize_t<DT, MODE, false, true>(s, x, rows, cols, o, ts, err, check_ts, st, d)
+                : launch_quantize_t<DT, MODE, false, false>(s, x, rows, cols, o, ts, err, check_ts, st, d);
+}
+
+template <int MODE>
+int quantize_t_entry(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                     const OutT &o, float *ts, int ts_mode, int *err_flag, void *stream)
+{
+    Shape s;
+    int rc = check_tensor(x, x_dtype, rows, cols, ld_x, s);
+    if (rc != IF4_OK) return rc;
+    if (rows % 16 != 0) return IF4_ERR_SHAPE;
+    if (ts_mode != IF4_TS_COMPUTE && ts_mode != IF4_TS_GIVEN) return IF4_ERR_MODE;
+    if (!ts || !o.codes != !o.scales) return IF4_ERR_NULL;
+    if (s.ngroups > 0 && (!o.codes_t || !o.scales_t)) return IF4_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(o.codes) % 16 || reinterpret_cast<uintptr_t>(o.codes_t) % 16 ||
+        reinterpret_cast<uintptr_t>(ts) % 4 || reinterpret_cast<uintptr_t>(err_flag) % 4)
+        return IF4_ERR_ALIGN;
+    DeviceInfo d;
+    rc = check_device(d);
+    if (rc != IF4_OK) return rc;
+    if (ts_mode == IF4_TS_COMPUTE) {
+        rc = if4_tensor_amax(x, x_dtype, rows, cols, ld_x, ts, err_flag, stream);
+        if (rc != IF4_OK) return rc;
+        rc = if4_tensor_scale(ts, ts, stream);
+        if (rc != IF4_OK) return rc;
+    }
+    if (s.ngroups == 0) return IF4_OK;
+    const int check_ts = ts_mode == IF4_TS_GIVEN ? 1 : 0;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (x_dtype) {
+    case IF4_F32:
+        return dispatch_quantize_t<DT_F32, MODE>(s, x, rows, cols, o, ts, err_flag, check_ts, st, d);
+    case IF4_BF16:
+        return dispatch_quantize_t<DT_BF16, MODE>(s, x, rows, cols, o, ts, err_flag, check_ts, st, d);
+    default:
+        return dispatch_quantize_t<DT_F16, MODE>(s, x, rows, cols, o, ts, err_flag, check_ts, st, d);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int if4_quantize_t(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                   uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, float *ts,
+                   int ts_mode, int *err_flag, void *stream)
+{
+    return quantize_t_entry<Q_IF4>(x, x_dtype, rows, cols, ld_x, {codes, scales, codes_t, scales_t},
+                                   ts, ts_mode, err_flag, stream);
+}
+
+int nvfp4_quantize_t(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                     uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                     float *ts, int ts_mode, int *err_flag, void *stream)
+{
+    return quantize_t_entry<Q_NVFP4>(x, x_dtype, rows, cols, ld_x,
+                                     {codes, scales, codes_t, scales_t}, ts, ts_mode, err_flag,
+                                     stream);
+}
+
+}  // extern "C"

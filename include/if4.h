@@ -384,6 +384,80 @@ int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, const float *a
                  void *c, int c_dtype, int *err_flag, void *stream);
 
 /*
+ * Quantizers along the rows: groups of 16 consecutive rows of one column, that
+ * is the quantization of x^T along its last axis, byte-identical to
+ * if4_quantize / nvfp4_quantize of a transposed copy under the same tensor
+ * scale.  The gradients of a linear contract over the axes its forward pass
+ * does not group, so a trained linear needs its operands both ways (W4A4
+ * training: companion, "Adaptive Block-Scaled Data Types for FP4 Training").
+ * codes / scales: both NULL, or the row form too ([rows, cols/2] and [rows,
+ * cols/16], as if4_quantize writes them), from the same pass over x.
+ *
+ * codes_t: uint8 [cols, rows/2], scales_t: uint8 [cols, rows/16], dense.
+ * rows % 16 == 0 and cols % 16 == 0 (IF4_ERR_SHAPE).  codes, codes_t 16-byte
+ * aligned; no output may overlap x.  ts_mode, ts, err_flag and the other rules
+ * as if4_quantize.
+ */
+int if4_quantize_t(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                   uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, float *ts,
+                   int ts_mode, int *err_flag, void *stream);
+int nvfp4_quantize_t(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                     uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                     float *ts, int ts_mode, int *err_flag, void *stream);
+
+/*
+ * RMS norm with the residual's addition and a 4-bit output: the producer of a
+ * quantized linear's activations.  Per row:
+ *   h    = RN(x + residual) in x_dtype (x itself without a residual)
+ *   rstd = fl(1 / sqrt(sum(h^2) / cols + eps)), the sum, the quotient and the root in
+ *          binary64, rounded once to binary32
+ *   y    = fl(fl(h * rstd) * weight), binary32
+ * and codes / scales are IF4 (or NVFP4) of y under the given tensor scale *ts
+ * (as if4_linear_quantized: known before y is, for example the previous
+ * step's; IF4_DEV_BAD_SCALE if invalid).  y itself is not stored.
+ *
+ * weight: [cols] of w_dtype, x_dtype or IF4_F32; 16-byte aligned.  residual,
+ * h, rstd, amax may be NULL.  h [rows, cols] receives h; it may be x's or the
+ * residual's own memory (with the same row stride), otherwise no output may
+ * overlap an input.  rstd: float [rows].  amax: a device float that is
+ * raised to max |y| (the caller zeroes it; if4_tensor_scale then gives the
+ * next step's ts).  eps finite and > 0 (IF4_ERR_MODE).  x, residual, h: 16-byte
+ * aligned, row strides in elements, ld*elem_size % 16 == 0.  Any number of
+ * columns with cols % 16 == 0.  Inf or NaN in y sets IF4_DEV_NONFINITE (that
+ * row's codes are unspecified).  Other rules as if4_quantize.
+ */
+int if4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, int64_t ld_res,
+                          const void *weight, int w_dtype, int x_dtype, int64_t rows, int64_t cols,
+                          float eps, void *h, int64_t ld_h, float *rstd, uint8_t *codes,
+                          uint8_t *scales, const float *ts, float *amax, int *err_flag,
+                          void *stream);
+int nvfp4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, int64_t ld_res,
+                            const void *weight, int w_dtype, int x_dtype, int64_t rows,
+                            int64_t cols, float eps, void *h, int64_t ld_h, float *rstd,
+                            uint8_t *codes, uint8_t *scales, const float *ts, float *amax,
+                            int *err_flag, void *stream);
+
+/*
+ * Gradient of that norm, the quantizer passing gradients straight through: with
+ * n = h * rstd and g = dy * weight,
+ *   dx = RN(dres + rstd * (g - n * mean(g * n))),  dweight = sum over rows of dy * n.
+ * dx is the gradient of x and of the residual alike.  dres, the gradient that
+ * reaches h past the norm, may be NULL.  dy, h, dres, dx [rows, cols] of
+ * x_dtype; h and rstd as the forward call wrote them; dweight float [cols],
+ * overwritten (zero for rows == 0).  Sums in binary32, in an order that does
+ * not change between calls.  dx may be dy's or dres's own memory (with the
+ * same row stride).  workspace: if4_rms_norm_backward_workspace_bytes (0 for
+ * invalid sizes), 256-byte aligned, one per call that may run at the same
+ * time.  Types, alignment and strides as the forward call.
+ */
+size_t if4_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t ld_h,
+                          const void *weight, int w_dtype, const float *rstd, const void *dres,
+                          int64_t ld_dres, int x_dtype, int64_t rows, int64_t cols, void *dx,
+                          int64_t ld_dx, float *dweight, void *workspace, size_t ws_bytes,
+                          void *stream);
+
+/*
  * IF6 and IF3: the same adaptive FP/INT choice at 6 and 3 bits per value.
  * The pages name both formats and say the adaptive choice carries over to
  * other bit widths ("Adaptive Block-Scaled Data Types", abstract; companion
