@@ -116,9 +116,15 @@ def _check(rc: int, name: str):
         raise IF4Error(f"{name}: {lib.if4_status_str(rc).decode()} (status {rc})")
 
 
+# the handle of a device's current stream, without the Stream object that
+# torch.cuda.current_stream() makes (0.1 against 3.1 us per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return _vp(s.cuda_stream)
+    if stream is None:
+        return _vp(_raw_stream(torch.cuda.current_device()))
+    return _vp(stream.cuda_stream)
 
 
 def _ptr(t):
@@ -360,28 +366,84 @@ def if4_linear_quantized(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, works
 
 
 # ------------------------------------------------- the NVFP4 linear layer ---
+#
+# These calls sit between single-token kernels of a few microseconds, so each
+# one checks its tensors with as few Python operations as will do (an expected
+# argument passes in one comparison chain; what is wrong is worked out only
+# when something is), and they run on the device of their tensors.
 
 def _device(name, *tensors):
-    """The CUDA device that every given tensor lives on (None entries skipped)."""
-    dev = None
+    """Index of the CUDA device that every given tensor lives on (None skipped)."""
+    dev = -2
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name}: every tensor must be on a CUDA device")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-        dev = t.device
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:                       # -1: not a CUDA tensor
+                    raise ValueError(f"{name}: every tensor must be on a CUDA device")
+                if dev >= 0:
+                    raise ValueError(f"{name}: tensors on cuda:{dev} and cuda:{d}")
+                dev = d
     return dev
 
 
+def _call(name, dev, stream, *args):
+    """The C entry point `name` with args and the stream (the device's current
+    one by default), with the tensors' device current."""
+    fn = getattr(lib, name)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc != IF4_OK:
+        _check(rc, name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _new(rows, cols, dtype, device):
+    # empty_strided: 1.5 us per call against torch.empty's 2.5
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _new1(n, dtype, device):
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
+def _dense(t, name, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
 def _word(t, name, dtype):
-    if t is not None and (t.dtype != dtype or t.numel() < 1):
+    if t is not None and (t.dtype is not dtype or t.numel() < 1):
         raise ValueError(f"{name} must be a {dtype} device tensor")
 
 
+def _rows(t, name, dtype=None, shape=None):
+    """A 2-D tensor whose rows are contiguous and do not overlap: its row
+    stride in elements."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be 2-D" + ("" if shape is None else f" of {tuple(shape)}"))
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return ld if rows > 1 and cols > 0 else cols
+
+
 def nvfp4_linear_workspace_bytes(M, N, K):
-    return int(lib.nvfp4_linear_workspace_bytes(int(M), int(N), int(K)))
+    return lib.nvfp4_linear_workspace_bytes(M, N, K)
+
+
+def _workspace(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, err_flag,
@@ -391,50 +453,34 @@ def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
     nvfp4_linear_workspace_bytes, or None where that is 0."""
     dev = _device("nvfp4_linear", a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
                   err_flag)
-    if a_codes.dim() != 2 or b_codes.dim() != 2 or c.dim() != 2:
-        raise ValueError("a_codes, b_codes and c must be 2-D")
-    M, K, N = a_codes.shape[0], a_codes.shape[1] * 2, b_codes.shape[0]
-    _u8(a_codes, "a_codes", (M, K // 2))
-    _u8(a_scales, "a_scales", (M, K // 16))
-    _u8(b_codes, "b_codes", (N, K // 2))
-    _u8(b_scales, "b_scales", (N, K // 16))
-    _word(a_ts, "a_ts", torch.float32)
-    _word(b_ts, "b_ts", torch.float32)
+    if a_codes.dim() != 2 or b_codes.dim() != 2:
+        raise ValueError("a_codes and b_codes must be 2-D")
+    (M, kb), N = a_codes.shape, b_codes.shape[0]
+    u8, f32 = torch.uint8, torch.float32
+    _dense(a_codes, "a_codes", u8, (M, kb))
+    _dense(a_scales, "a_scales", u8, (M, kb // 8))
+    _dense(b_codes, "b_codes", u8, (N, kb))
+    _dense(b_scales, "b_scales", u8, (N, kb // 8))
+    _dense(c, "c", c.dtype, (M, N))
+    _word(a_ts, "a_ts", f32)
+    _word(b_ts, "b_ts", f32)
     _word(err_flag, "err_flag", torch.int32)
-    if tuple(c.shape) != (M, N) or not c.is_contiguous():
-        raise ValueError(f"c must be a contiguous tensor of shape {(M, N)}")
-    with torch.cuda.device(dev):
-        _check(lib.nvfp4_linear(_ptr(a_codes), _ptr(a_scales), _ptr(a_ts), _ptr(b_codes),
-                                _ptr(b_scales), _ptr(b_ts), M, N, K, _ptr(workspace),
-                                0 if workspace is None else
-                                workspace.numel() * workspace.element_size(), _ptr(c),
-                                _dtype(c, "c"), _ptr(err_flag), _stream(stream)), "nvfp4_linear")
+    _call("nvfp4_linear", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), a_ts.data_ptr(),
+          b_codes.data_ptr(), b_scales.data_ptr(), b_ts.data_ptr(), M, N, 2 * kb,
+          *_workspace(workspace), c.data_ptr(), _dtype(c, "c"), _at(err_flag))
 
 
 def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
     """a, b: (codes, scales, ts) of NVFP4 operands [M, K] and [N, K].  Returns
     A B^T [M, N] of dtype."""
-    dev, M, N = a[0].device, a[0].shape[0], b[0].shape[0]
-    c = torch.empty((M, N), dtype=dtype, device=dev)
+    (M, kb), N, dev = a[0].shape, b[0].shape[0], a[0].device
+    c = _new(M, N, dtype, dev)
     if err_flag is None:
         err_flag = torch.zeros(1, dtype=torch.int32, device=dev)
-    need = nvfp4_linear_workspace_bytes(M, N, a[0].shape[1] * 2)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    need = lib.nvfp4_linear_workspace_bytes(M, N, 2 * kb)
+    ws = _new1(need, torch.uint8, dev) if need else None
     nvfp4_linear(*a, *b, ws, c, err_flag, stream)
     return c
-
-
-def _rows(t, name, dtype=None, shape=None):
-    """A 2-D tensor whose rows are contiguous and do not overlap: its row
-    stride in elements."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be 2-D" + ("" if shape is None else f" of {tuple(shape)}"))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.stride(0) if rows > 1 and cols > 0 else cols
 
 
 def _entry(mode, name):
@@ -449,17 +495,17 @@ def _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, er
     rows, cols = x.shape
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales go together")
+    u8 = torch.uint8
     if codes is not None:
-        _u8(codes, "codes", (rows, cols // 2))
-        _u8(scales, "scales", (rows, cols // 16))
-    _u8(codes_t, "codes_t", (cols, rows // 2))
-    _u8(scales_t, "scales_t", (cols, rows // 16))
+        _dense(codes, "codes", u8, (rows, cols // 2))
+        _dense(scales, "scales", u8, (rows, cols // 16))
+    _dense(codes_t, "codes_t", u8, (cols, rows // 2))
+    _dense(scales_t, "scales_t", u8, (cols, rows // 16))
     _word(ts, "ts", torch.float32)
     _word(err_flag, "err_flag", torch.int32)
-    with torch.cuda.device(dev):
-        _check(getattr(lib, entry)(_ptr(x), _dtype(x, "x"), rows, cols, ld, _ptr(codes),
-                                   _ptr(scales), _ptr(codes_t), _ptr(scales_t), _ptr(ts),
-                                   int(ts_mode), _ptr(err_flag), _stream(stream)), entry)
+    _call(entry, dev, stream, x.data_ptr(), _dtype(x, "x"), rows, cols, ld, _at(codes),
+          _at(scales), codes_t.data_ptr(), scales_t.data_ptr(), ts.data_ptr(), ts_mode,
+          _at(err_flag))
 
 
 def if4_quantize_t(x, codes, scales, codes_t, scales_t, ts, ts_mode=TS_COMPUTE, err_flag=None,
@@ -484,50 +530,46 @@ def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=No
     computes it; a float32 tensor is used as given."""
     entry = _entry(mode, "quantize_t")
     _rows(x, "x")
-    (rows, cols), dev = x.shape, x.device
-    u8 = dict(dtype=torch.uint8, device=dev)
-    codes_t, scales_t = torch.empty((cols, rows // 2), **u8), torch.empty((cols, rows // 16), **u8)
-    codes = torch.empty((rows, cols // 2), **u8) if with_rows else None
-    scales = torch.empty((rows, cols // 16), **u8) if with_rows else None
-    if ts is None:
-        ts_t, ts_mode = torch.empty(1, dtype=torch.float32, device=dev), TS_COMPUTE
-    else:
-        ts_t, ts_mode = ts, TS_GIVEN
-    _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts_t, ts_mode, err_flag, stream)
+    (rows, cols), dev, u8 = x.shape, x.device, torch.uint8
+    codes_t, scales_t = _new(cols, rows // 2, u8, dev), _new(cols, rows // 16, u8, dev)
+    codes = scales = None
     if with_rows:
-        return codes, scales, codes_t, scales_t, ts_t
-    return codes_t, scales_t, ts_t
+        codes, scales = _new(rows, cols // 2, u8, dev), _new(rows, cols // 16, u8, dev)
+    if ts is None:
+        ts, ts_mode = _new1(1, torch.float32, dev), TS_COMPUTE
+    else:
+        ts_mode = TS_GIVEN
+    _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream)
+    if with_rows:
+        return codes, scales, codes_t, scales_t, ts
+    return codes_t, scales_t, ts
 
 
 def _norm_weight(weight, cols, dtype):
-    if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous():
+    if weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous tensor of {cols} elements")
-    if weight.dtype not in (dtype, torch.float32):
+    if weight.dtype is not dtype and weight.dtype is not torch.float32:
         raise ValueError(f"weight must be {dtype} or float32")
 
 
 def _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
                    stream):
     dev = _device(entry, x, residual, weight, h, rstd, codes, scales, ts, amax, err_flag)
-    ld = _rows(x, "x")
-    rows, cols = x.shape
-    ld_res = 0 if residual is None else _rows(residual, "residual", x.dtype, x.shape)
-    ld_h = 0 if h is None else _rows(h, "h", x.dtype, x.shape)
-    _norm_weight(weight, cols, x.dtype)
-    _u8(codes, "codes", (rows, cols // 2))
-    _u8(scales, "scales", (rows, cols // 16))
-    if rstd is not None and (rstd.dtype != torch.float32 or tuple(rstd.shape) != (rows,)
-                             or not rstd.is_contiguous()):
-        raise ValueError(f"rstd must be a contiguous float32 tensor of {rows} elements")
+    ld, shape, dtype = _rows(x, "x"), x.shape, x.dtype
+    rows, cols = shape
+    ld_res = 0 if residual is None else _rows(residual, "residual", dtype, shape)
+    ld_h = 0 if h is None else _rows(h, "h", dtype, shape)
+    _norm_weight(weight, cols, dtype)
+    _dense(codes, "codes", torch.uint8, (rows, cols // 2))
+    _dense(scales, "scales", torch.uint8, (rows, cols // 16))
+    if rstd is not None:
+        _dense(rstd, "rstd", torch.float32, (rows,))
     _word(ts, "ts", torch.float32)
     _word(amax, "amax", torch.float32)
     _word(err_flag, "err_flag", torch.int32)
-    with torch.cuda.device(dev):
-        _check(getattr(lib, entry)(_ptr(x), ld, _ptr(residual), ld_res, _ptr(weight),
-                                   _dtype(weight, "weight"), _dtype(x, "x"), rows, cols,
-                                   float(eps), _ptr(h), ld_h, _ptr(rstd), _ptr(codes),
-                                   _ptr(scales), _ptr(ts), _ptr(amax), _ptr(err_flag),
-                                   _stream(stream)), entry)
+    _call(entry, dev, stream, x.data_ptr(), ld, _at(residual), ld_res, weight.data_ptr(),
+          _dtype(weight, "weight"), _dtype(x, "x"), rows, cols, eps, _at(h), ld_h, _at(rstd),
+          codes.data_ptr(), scales.data_ptr(), ts.data_ptr(), _at(amax), _at(err_flag))
 
 
 def if4_rms_norm_quantize(x, residual, weight, eps, h, rstd, codes, scales, ts, amax=None,
@@ -554,51 +596,42 @@ def rms_norm_quantize(x, weight, ts, residual=None, eps=1e-6, mode="if4", amax=N
     entry = _entry(mode, "rms_norm_quantize")
     _rows(x, "x")
     (rows, cols), dev = x.shape, x.device
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    h = None if residual is None else torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    codes, scales = _new(rows, cols // 2, torch.uint8, dev), _new(rows, cols // 16, torch.uint8, dev)
+    rstd = _new1(rows, torch.float32, dev)
+    h = None if residual is None else _new(rows, cols, x.dtype, dev)
     _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
                    stream)
     return codes, scales, x if h is None else h, rstd
 
 
 def if4_rms_norm_backward_workspace_bytes(rows, cols):
-    return int(lib.if4_rms_norm_backward_workspace_bytes(int(rows), int(cols)))
+    return lib.if4_rms_norm_backward_workspace_bytes(rows, cols)
 
 
 def if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, workspace, stream=None):
     """Gradient of the norm into dx (x's type) and dweight (float32 [cols])."""
     name = "if4_rms_norm_backward"
     dev = _device(name, dy, h, weight, rstd, dres, dx, dweight, workspace)
-    rows, cols = h.shape if h.dim() == 2 else (0, 0)
-    ld_h = _rows(h, "h")
-    ld_dy = _rows(dy, "dy", h.dtype, h.shape)
-    ld_dx = _rows(dx, "dx", h.dtype, h.shape)
-    ld_dres = 0 if dres is None else _rows(dres, "dres", h.dtype, h.shape)
-    _norm_weight(weight, cols, h.dtype)
-    for t, n, k in ((rstd, "rstd", rows), (dweight, "dweight", cols)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (k,) or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous float32 tensor of {k} elements")
-    with torch.cuda.device(dev):
-        _check(lib.if4_rms_norm_backward(_ptr(dy), ld_dy, _ptr(h), ld_h, _ptr(weight),
-                                         _dtype(weight, "weight"), _ptr(rstd), _ptr(dres), ld_dres,
-                                         _dtype(h, "h"), rows, cols, _ptr(dx), ld_dx,
-                                         _ptr(dweight), _ptr(workspace),
-                                         0 if workspace is None else
-                                         workspace.numel() * workspace.element_size(),
-                                         _stream(stream)), name)
+    ld_h, shape, dtype = _rows(h, "h"), h.shape, h.dtype
+    rows, cols = shape
+    ld_dy, ld_dx = _rows(dy, "dy", dtype, shape), _rows(dx, "dx", dtype, shape)
+    ld_dres = 0 if dres is None else _rows(dres, "dres", dtype, shape)
+    _norm_weight(weight, cols, dtype)
+    _dense(rstd, "rstd", torch.float32, (rows,))
+    _dense(dweight, "dweight", torch.float32, (cols,))
+    _call(name, dev, stream, dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(),
+          _dtype(weight, "weight"), rstd.data_ptr(), _at(dres), ld_dres, _dtype(h, "h"), rows, cols,
+          dx.data_ptr(), ld_dx, dweight.data_ptr(), *_workspace(workspace))
 
 
 def rms_norm_backward(dy, h, weight, rstd, dres=None, stream=None):
     """Gradient of rms_norm_quantize (straight through the quantizer) from dy,
     the gradient of the norm's output, and dres, that of h past the norm.
     Returns (dx, dweight): dx for x and the residual alike, dweight float32."""
-    rows, cols = h.shape
-    dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
-    dweight = torch.empty(cols, dtype=torch.float32, device=h.device)
-    need = if4_rms_norm_backward_workspace_bytes(rows, cols)
-    ws = torch.empty(need, dtype=torch.uint8, device=h.device) if need else None
+    (rows, cols), dev = h.shape, h.device
+    dx, dweight = _new(rows, cols, h.dtype, dev), _new1(cols, torch.float32, dev)
+    need = lib.if4_rms_norm_backward_workspace_bytes(rows, cols)
+    ws = _new1(need, torch.uint8, dev) if need else None
     if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, ws, stream)
     return dx, dweight
 

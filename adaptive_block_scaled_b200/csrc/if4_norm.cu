@@ -72,8 +72,6 @@ __device__ __forceinline__ void store_group(char *p, const Raw<DT> &r)
         st_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
 }
 
-// Plain (coherent) 16-byte loads: h may be x's or the residual's own memory,
-// so these inputs are not read through the read-only path.
 template <int DT>
 __device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r)
 {
@@ -111,29 +109,236 @@ struct NormArgs {
     int *err;
     int64_t rows;
     int gpr;                        // groups per row
-    float eps;
+    bool v8;                        // x, residual and h on 32-byte boundaries
+    double inv_cols, eps;
 };
+
+// rstd of a row from its binary64 sum of squares.  The binary32 reciprocal root
+// (2^-22 off at most) and two Newton steps in binary64 leave 2^-52, so the one
+// rounding to binary32 is the rounding of the definition's value (which has
+// the same freedom in its last binary64 bits); the division and root in
+// binary64 took as long as a sixth of the row.  Outside binary32's comfortable
+// range they are used as they stand.
+__device__ __noinline__ float row_rstd_general(double v) { return (float)(1.0 / sqrt(v)); }
+
+__device__ __forceinline__ float row_rstd(double s, double inv_cols, double eps)
+{
+    const double v = fma(s, inv_cols, eps);
+    if (!(v > 1e-30 && v < 1e30)) return row_rstd_general(v);
+    double r = (double)rsqrtf((float)v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = fma(r * 0.5, fma(-v * r, r, 1.0), r);
+    return (float)r;
+}
+
+// 256-bit (32-byte aligned addresses) or 128-bit coherent loads and stores of
+// one group, past L1: h may be x's or the residual's own memory, so these are
+// not read through the read-only path.
+template <int DT>
+__device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r, bool v8)
+{
+    if (v8) {
+#pragma unroll
+        for (int q = 0; q < (DT == DT_F32 ? 2 : 1); ++q)
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(r.w[8 * q]), "=r"(r.w[8 * q + 1]), "=r"(r.w[8 * q + 2]),
+                           "=r"(r.w[8 * q + 3]), "=r"(r.w[8 * q + 4]), "=r"(r.w[8 * q + 5]),
+                           "=r"(r.w[8 * q + 6]), "=r"(r.w[8 * q + 7])
+                         : "l"(p + 32 * q));
+    } else {
+        load_group_rw<DT>(p, r);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_group(char *p, const Raw<DT> &r, bool v8)
+{
+    if (v8) {
+#pragma unroll
+        for (int q = 0; q < (DT == DT_F32 ? 2 : 1); ++q)
+            st_v8(p + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(r.w + 8 * q));
+    } else {
+        store_group<DT>(p, r);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void zero_group(Raw<DT> &r)
+{
+#pragma unroll
+    for (uint32_t &w : r.w) w = 0u;
+}
+
+// A group of the weight, kept in L1 for the next rows.
+template <int WT>
+__device__ __forceinline__ void load_weight(const char *w, int g, Raw<WT> &r)
+{
+    const char *p = w + (int64_t)g * 16 * elem_bytes<WT>();
+#pragma unroll
+    for (int q = 0; q < (WT == DT_F32 ? 4 : 2); ++q)
+        asm("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+            : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
+            : "l"(p + 16 * q));
+}
+
+// h = RN(x + r), into x.
+template <int DT>
+__device__ __forceinline__ void add_residual(Raw<DT> &x, const Raw<DT> &r)
+{
+    f2_t u[8], v[8];
+    to_pairs<DT>(x, u);
+    to_pairs<DT>(r, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = f2_add(u[j], v[j]);
+    to_raw<DT>(u, x);
+}
 
 // h of one group: x, or RN(x + residual).
 template <int DT>
 __device__ __forceinline__ void load_h(const NormArgs &a, int64_t row, int g, Raw<DT> &h)
 {
     constexpr int GB = 16 * elem_bytes<DT>();
-    load_group_rw<DT>(a.x + row * a.ld_x + (int64_t)g * GB, h);
+    load_group_rw<DT>(a.x + row * a.ld_x + (int64_t)g * GB, h, a.v8);
     if (a.res) {
         Raw<DT> r;
-        load_group_rw<DT>(a.res + row * a.ld_res + (int64_t)g * GB, r);
-        f2_t u[8], v[8];
-        to_pairs<DT>(h, u);
-        to_pairs<DT>(r, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = f2_add(u[j], v[j]);
-        to_raw<DT>(u, h);
+        load_group_rw<DT>(a.res + row * a.ld_res + (int64_t)g * GB, r, a.v8);
+        add_residual<DT>(h, r);
     }
 }
 
-// Any number of columns: a block per row, h formed twice (the second time
-// mostly from L2).
+// Rows of up to G groups per thread of the block: one pass, h kept in
+// registers between the sum and the encode (the weight comes from L1 each
+// time).  A block takes rows blockIdx.x, + gridDim.x, ...; with one or two
+// groups per thread, the next row's loads are issued as soon as h of a row is
+// formed (more groups leave no registers for it).
+template <int DT, int G>
+constexpr int norm_blocks_per_sm()
+{
+    return G == 1 ? (DT == DT_F32 ? 3 : 4) : G == 2 ? 2 : 1;
+}
+
+template <int DT, int WT, int MODE, int G>
+__global__ void __launch_bounds__(G == 4 ? 512 : 256, norm_blocks_per_sm<DT, G>())
+rms_norm_quantize_rows_kernel(const __grid_constant__ NormArgs a)
+{
+    pdl_enter();
+    __shared__ float inv_tab[128];
+    __shared__ double sums[2][16];
+    constexpr int GB = 16 * elem_bytes<DT>();
+    const float ts = *a.ts;
+    const float rts = __frcp_rn(ts);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && a.err)
+        atomicOr(a.err, IF4_DEV_BAD_SCALE);
+    for (int i = threadIdx.x; i < 128; i += blockDim.x)
+        inv_tab[i] = i == 0 ? 0.0f : __frcp_rn(__fmul_rn(f32_from_e4m3(i), ts));
+    constexpr bool PREFETCH = G == 1 || (G == 2 && DT != DT_F32);
+    Raw<DT> x[PREFETCH ? G : 1], r[PREFETCH ? G : 1];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < (PREFETCH ? G : 0); ++k) {
+            const int g = threadIdx.x + k * blockDim.x;
+            if (g < a.gpr) {
+                load_group_rw<DT>(a.x + row * a.ld_x + (int64_t)g * GB, x[k], a.v8);
+                if (a.res) load_group_rw<DT>(a.res + row * a.ld_res + (int64_t)g * GB, r[k], a.v8);
+            }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < (PREFETCH ? G : 0); ++k) {
+        zero_group(x[k]);
+        zero_group(r[k]);
+    }
+    bool nonfinite = false;
+    uint32_t top = 0;
+    int par = 0;
+    const int warps = blockDim.x >> 5;
+    int64_t row = blockIdx.x;
+    if (PREFETCH && row < a.rows) fetch(row);
+    __syncthreads();                        // inv_tab
+    for (; row < a.rows; row += gridDim.x, par ^= 1) {
+        double s = 0.0;
+        Raw<DT> h[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            if constexpr (PREFETCH) {
+                h[k] = x[k];
+                if (a.res) add_residual<DT>(h[k], r[k]);
+            } else {
+                const int g = threadIdx.x + k * blockDim.x;
+                zero_group(h[k]);
+                if (g < a.gpr) load_h<DT>(a, row, g, h[k]);
+            }
+            f2_t v[8];
+            to_pairs<DT>(h[k], v);
+            double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float lo, hi;
+                f2_unpack(v[j], lo, hi);
+                s0 = fma((double)lo, (double)lo, s0);
+                s1 = fma((double)hi, (double)hi, s1);
+            }
+            s += s0 + s1;
+        }
+        // h may be x's or the residual's memory: this row's store only comes
+        // after this row's loads, and no other block reads this row
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int g = threadIdx.x + k * blockDim.x;
+            if (a.h && g < a.gpr)
+                store_group<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h[k], a.v8);
+        }
+        if (PREFETCH && row + gridDim.x < a.rows) fetch(row + gridDim.x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (warps > 1) {
+            // two buffers in turn: a warp writes row i + 2's only after the
+            // barrier of row i + 1, which every reader of row i's has passed
+            if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = s;
+            __syncthreads();
+            s = sums[par][0];
+            for (int i = 1; i < warps; ++i) s += sums[par][i];
+        }
+        const float rstd = row_rstd(s, a.inv_cols, a.eps);
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+        const f2_t RS = f2_pack(rstd, rstd);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int g = threadIdx.x + k * blockDim.x;
+            if (g < a.gpr) {
+                f2_t v[8], wv[8];
+                Raw<WT> w;
+                load_weight<WT>(a.w, g, w);
+                to_pairs<DT>(h[k], v);
+                to_pairs<WT>(w, wv);
+                uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = f2_mul(f2_mul(v[j], RS), wv[j]);
+                    float lo, hi;
+                    f2_unpack(v[j], lo, hi);
+                    m0 = absmax_f32(m0, lo);
+                    m1 = absmax_f32(m1, hi);
+                }
+                const uint32_t m = absmax_f32(m0, __uint_as_float(m1)) & 0x7FFFFFFFu;
+                nonfinite |= m >= 0x7F800000u;
+                top = max(top, m);
+                const GroupCode c = encode_registers<MODE>(v, __uint_as_float(m), ts, rts, inv_tab);
+                const int64_t gi = row * a.gpr + g;
+                st_v2(a.codes + gi * 8, c.c0, c.c1);
+                st_u8(a.scales + gi, c.scale);
+            }
+        }
+    }
+    if (a.amax) {
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if ((threadIdx.x & 31) == 0) atomicMax(a.amax, top);
+    }
+    if (nonfinite && a.err) atomicOr(a.err, IF4_DEV_NONFINITE);
+}
+
+// More columns than the rows kernel holds in registers: a block per row, h
+// formed twice (the second time mostly from L2).
 template <int DT, int WT, int MODE>
 __global__ void __launch_bounds__(NORM_THREADS)
 rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
@@ -165,7 +370,7 @@ rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
             }
         }
         s = block_sum(s, sums);
-        const float rstd = (float)(1.0 / sqrt(s / (double)(a.gpr * 16.0) + (double)a.eps));
+        const float rstd = row_rstd(s, a.inv_cols, a.eps);
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
         const f2_t RS = f2_pack(rstd, rstd);
         for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
@@ -214,9 +419,136 @@ struct BackArgs {
     float *part;                    // [BACK_BLOCKS][cols]
     int64_t rows;
     int gpr;
+    bool v8;                        // every matrix on 32-byte boundaries
+    float inv_cols;
 };
 
-// dx, any number of columns: a block per row, dy and h read twice.
+// Rows of up to 1024 groups (G per thread): one pass over dy, h and dres.  A
+// block of 512 threads holds 512 / T rows at a time, T threads each (a power
+// of two, at least a warp); a thread keeps its columns' part of dw in
+// registers over all its rows.  The row sums meet at a barrier of the row's
+// own threads.  At the end the block's row slots add their parts through
+// shared memory, and the block writes one partial row.
+template <int DT, int WT, int G>
+__global__ void __launch_bounds__(512, G == 1 && DT != DT_F32 ? 2 : 1)
+rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
+{
+    pdl_enter();
+    constexpr int GB = 16 * elem_bytes<DT>();
+    __shared__ float sums[2][16];
+    extern __shared__ float slot_dw[];              // [slots - 1][cols]
+    const int slots = 512 / T, slot = threadIdx.x / T, t = threadIdx.x % T;
+    const int warps = T >> 5, warp0 = slot * warps;
+    f2_t dw[G][8];
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[k][j] = f2_pack(0.0f, 0.0f);
+    int par = 0;
+    for (int64_t row = (int64_t)blockIdx.x * slots + slot; row < a.rows;
+         row += (int64_t)gridDim.x * slots, par ^= 1) {
+        const float rstd = a.rstd[row];
+        Raw<DT> h[G], d[G], e[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int g = t + k * T;
+            zero_group(h[k]);
+            zero_group(d[k]);
+            zero_group(e[k]);
+            if (g < a.gpr) {
+                load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h[k], a.v8);
+                load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, d[k], a.v8);
+                if (a.dres)
+                    load_group_rw<DT>(a.dres + row * a.ld_dres + (int64_t)g * GB, e[k], a.v8);
+            }
+        }
+        f2_t acc = f2_pack(0.0f, 0.0f);
+        const f2_t RS = f2_pack(rstd, rstd);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            f2_t hv[8], dv[8], wv[8];
+            Raw<WT> w;
+            load_weight<WT>(a.w, min(t + k * T, a.gpr - 1), w);
+            to_pairs<DT>(h[k], hv);
+            to_pairs<DT>(d[k], dv);
+            to_pairs<WT>(w, wv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const f2_t dh = f2_mul(dv[j], hv[j]);
+                acc = f2_fma(dh, wv[j], acc);
+                dw[k][j] = f2_fma(dh, RS, dw[k][j]);
+            }
+        }
+        float s, hi;
+        f2_unpack(acc, s, hi);
+        s += hi;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (warps > 1) {
+            // two buffers in turn: see the forward kernel
+            if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = s;
+            asm volatile("bar.sync %0, %1;" :: "r"(slot + 1), "r"(T) : "memory");
+            s = sums[par][warp0];
+            for (int i = 1; i < warps; ++i) s += sums[par][warp0 + i];
+        }
+        // mean(g * n) * rstd, n = h * rstd
+        const float c = s * rstd * rstd * a.inv_cols;
+        const f2_t NC = f2_pack(-c, -c);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int g = t + k * T;
+            if (g < a.gpr) {
+                f2_t hv[8], dv[8], wv[8], ev[8];
+                Raw<WT> w;
+                load_weight<WT>(a.w, g, w);
+                to_pairs<DT>(h[k], hv);
+                to_pairs<DT>(d[k], dv);
+                to_pairs<WT>(w, wv);
+                to_pairs<DT>(e[k], ev);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const f2_t v = f2_mul(f2_fma(hv[j], NC, f2_mul(dv[j], wv[j])), RS);
+                    dv[j] = a.dres ? f2_add(v, ev[j]) : v;
+                }
+                Raw<DT> o;
+                to_raw<DT>(dv, o);
+                store_group<DT>(a.dx + row * a.ld_dx + (int64_t)g * GB, o, a.v8);
+            }
+        }
+    }
+    // the block's partial row: slot 0 adds the others' in order
+    const int cols = a.gpr * 16;
+    if (slots > 1) {
+        if (slot > 0)
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const int g = t + k * T;
+                if (g < a.gpr)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<f2_t *>(slot_dw + (slot - 1) * cols + g * 16 + 2 * j) = dw[k][j];
+            }
+        __syncthreads();
+    }
+    if (slot == 0)
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int g = t + k * T;
+            if (g < a.gpr) {
+                for (int q = 0; q < slots - 1; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dw[k][j] = f2_add(dw[k][j], *reinterpret_cast<const f2_t *>(
+                                                        slot_dw + q * cols + g * 16 + 2 * j));
+                float *p = a.part + (int64_t)blockIdx.x * cols + g * 16;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) *reinterpret_cast<f2_t *>(p + 2 * j) = dw[k][j];
+            }
+        }
+}
+
+// More columns than the rows kernel holds: dx with a block per row, dy and h
+// read twice, and dw's partial sums by a kernel of their own.
 template <int DT, int WT>
 __global__ void __launch_bounds__(NORM_THREADS)
 rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
@@ -246,7 +578,7 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
         }
         s = block_sum(s, sums);
         // mean(g * n) * rstd, n = h * rstd
-        const float k = s * rstd * rstd / (float)(a.gpr * 16);
+        const float k = s * rstd * rstd * a.inv_cols;
         const f2_t RS = f2_pack(rstd, rstd), NK = f2_pack(-k, -k);
         for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
             Raw<DT> hr, dr, er;
@@ -298,16 +630,26 @@ rms_norm_dw_kernel(const __grid_constant__ BackArgs a)
     a.part[(int64_t)blockIdx.x * a.gpr * 16 + col] = s;
 }
 
-// dw: the partial sums in order.
-__global__ void __launch_bounds__(256)
+// dw: n partial rows.  A block takes 32 columns; warp v adds rows v, v + 32,
+// ..., then one warp adds the 32 sums in order.
+__global__ void __launch_bounds__(1024)
 rms_norm_dw_sum_kernel(const float *__restrict__ part, int n, int cols, float *__restrict__ dw)
 {
     pdl_enter();
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col >= cols) return;
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, v = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int i = 0; i < n; ++i) s += part[(int64_t)i * cols + col];
-    dw[col] = s;
+    if (col < cols)
+        for (int i = v; i < n; i += 32) s += part[(int64_t)i * cols + col];
+    sums[v][lane] = s;
+    __syncthreads();
+    if (v == 0 && col < cols) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += sums[i][lane];
+        dw[col] = s;
+    }
 }
 
 // ------------------------------------------------------------ host side ----
@@ -357,11 +699,27 @@ int rms_norm_quantize_entry(const void *x, int64_t ld_x, const void *res, int64_
     const NormArgs a{static_cast<const char *>(x), static_cast<const char *>(res),
                      static_cast<const char *>(w), static_cast<char *>(h), s.ld_bytes, sr.ld_bytes,
                      sh.ld_bytes, codes, scales, ts, rstd, reinterpret_cast<unsigned int *>(amax),
-                     err_flag, rows, (int)(cols / 16), eps};
+                     err_flag, rows, (int)(cols / 16),
+                     s.v8 && (!res || sr.v8) && (!h || sh.v8), 1.0 / (double)cols, (double)eps};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t n = cols / 16;
     return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
-        auto k = rms_norm_quantize_kernel<decltype(dt)::value, decltype(wt)::value, MODE>;
-        const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8);
-        return launch_k(k, grid, NORM_THREADS, static_cast<cudaStream_t>(stream), a);
+        constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
+        const int64_t warps = (n + 31) / 32;
+        auto rows_kernel = [&](auto k, auto G) {
+            constexpr int g = decltype(G)::value, per_sm = norm_blocks_per_sm<DT, g>();
+            // the fewest whole warps that hold a row; blocks for one wave
+            const unsigned threads = (unsigned)((warps + g - 1) / g * 32);
+            const int64_t wave = (int64_t)d.sm_count * per_sm * (256 / threads ? 256 / threads : 1);
+            return launch_k(k, (unsigned)std::min(rows, wave), threads, st, a);
+        };
+        if (n <= 256) return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 1>, std::integral_constant<int, 1>{});
+        if (n <= 512) return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 2>, std::integral_constant<int, 2>{});
+        if (n <= (DT == DT_F32 ? 1024 : 2048))
+            return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 4>, std::integral_constant<int, 4>{});
+        return launch_k(rms_norm_quantize_kernel<DT, WT, MODE>,
+                        (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8),
+                        (unsigned)NORM_THREADS, st, a);
     });
 }
 
@@ -427,20 +785,48 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
     const BackArgs a{static_cast<const char *>(dy), static_cast<const char *>(h),
                      static_cast<const char *>(weight), static_cast<const char *>(dres),
                      static_cast<char *>(dx), sy.ld_bytes, sh.ld_bytes, sr.ld_bytes, sx.ld_bytes,
-                     rstd, static_cast<float *>(workspace), rows, (int)(cols / 16)};
-    const int parts = (int)std::min<int64_t>(rows, BACK_BLOCKS);
+                     rstd, static_cast<float *>(workspace), rows, (int)(cols / 16),
+                     sy.v8 && sh.v8 && sx.v8 && (!dres || sr.v8), 1.0f / (float)cols};
+    const int64_t n = cols / 16;
+    auto sum_dw = [&](int parts) {
+        return launch_k(rms_norm_dw_sum_kernel, (unsigned)((cols + 31) / 32), 1024u, st,
+                        (const float *)workspace, parts, (int)cols, dweight);
+    };
     return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
         constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
+        if (n <= 1024) {
+            int T = 32;
+            while (T < 512 && T < n) T *= 2;
+            const int slots = 512 / T;
+            const int parts = (int)std::min<int64_t>((rows + slots - 1) / slots, BACK_BLOCKS);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)parts, 1, 1);
+            cfg.blockDim = dim3(512, 1, 1);
+            cfg.dynamicSmemBytes = (size_t)(slots - 1) * (size_t)cols * sizeof(float);
+            cfg.stream = st;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            const cudaError_t e =
+                n <= 512 ? cudaLaunchKernelEx(&cfg, rms_norm_backward_rows_kernel<DT, WT, 1>, a, T)
+                         : cudaLaunchKernelEx(&cfg, rms_norm_backward_rows_kernel<DT, WT, 2>, a, T);
+            if (e != cudaSuccess) return (int)IF4_ERR_CUDA;
+            return sum_dw(parts);
+        }
+        const int parts = (int)std::min<int64_t>(rows, BACK_BLOCKS);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)parts, (unsigned)((cols + 255) / 256), 1);
         cfg.blockDim = dim3(256, 1, 1);
         cfg.stream = st;
-        if (cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel<DT>, a) != cudaSuccess) return (int)IF4_ERR_CUDA;
-        int r = launch_k(rms_norm_dw_sum_kernel, (unsigned)((cols + 255) / 256), 256u, st,
-                         (const float *)workspace, parts, (int)cols, dweight);
+        if (cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel<DT>, a) != cudaSuccess)
+            return (int)IF4_ERR_CUDA;
+        const int r = sum_dw(parts);
         if (r != IF4_OK) return r;
-        const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8);
-        return launch_k(rms_norm_dx_kernel<DT, WT>, grid, (unsigned)NORM_THREADS, st, a);
+        return launch_k(rms_norm_dx_kernel<DT, WT>,
+                        (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8),
+                        (unsigned)NORM_THREADS, st, a);
     });
 }
 
