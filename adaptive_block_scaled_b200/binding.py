@@ -442,17 +442,10 @@ def nvfp4_linear_workspace_bytes(M, N, K):
     return lib.nvfp4_linear_workspace_bytes(M, N, K)
 
 
-def _workspace(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-
-
-def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, err_flag,
-                 stream=None):
-    """C = A B^T of NVFP4 operands on the block-scaled tensor cores, into the
-    dense c [M, N] (bf16, f16 or f32).  workspace: a uint8 tensor of
-    nvfp4_linear_workspace_bytes, or None where that is 0."""
-    dev = _device("nvfp4_linear", a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
-                  err_flag)
+def _nvfp4_linear(a, b, ws, c, err_flag, stream):
+    """Checks the operands (not c and ws) and calls nvfp4_linear."""
+    (a_codes, a_scales, a_ts), (b_codes, b_scales, b_ts) = a, b
+    dev = _device("nvfp4_linear", a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, c, err_flag)
     if a_codes.dim() != 2 or b_codes.dim() != 2:
         raise ValueError("a_codes and b_codes must be 2-D")
     (M, kb), N = a_codes.shape, b_codes.shape[0]
@@ -461,13 +454,24 @@ def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
     _dense(a_scales, "a_scales", u8, (M, kb // 8))
     _dense(b_codes, "b_codes", u8, (N, kb))
     _dense(b_scales, "b_scales", u8, (N, kb // 8))
-    _dense(c, "c", c.dtype, (M, N))
     _word(a_ts, "a_ts", f32)
     _word(b_ts, "b_ts", f32)
     _word(err_flag, "err_flag", torch.int32)
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     _call("nvfp4_linear", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), a_ts.data_ptr(),
-          b_codes.data_ptr(), b_scales.data_ptr(), b_ts.data_ptr(), M, N, 2 * kb,
-          *_workspace(workspace), c.data_ptr(), _dtype(c, "c"), _at(err_flag))
+          b_codes.data_ptr(), b_scales.data_ptr(), b_ts.data_ptr(), M, N, 2 * kb, wp, wn,
+          c.data_ptr(), _dtype(c, "c"), _at(err_flag))
+
+
+def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, err_flag,
+                 stream=None):
+    """C = A B^T of NVFP4 operands on the block-scaled tensor cores, into the
+    dense c [M, N] (bf16, f16 or f32).  workspace: a uint8 tensor of
+    nvfp4_linear_workspace_bytes, or None where that is 0."""
+    _device("nvfp4_linear", a_codes, workspace, c)
+    _dense(c, "c", c.dtype, (a_codes.shape[0], b_codes.shape[0]))
+    _nvfp4_linear((a_codes, a_scales, a_ts), (b_codes, b_scales, b_ts), workspace, c, err_flag,
+                  stream)
 
 
 def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
@@ -479,7 +483,7 @@ def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
         err_flag = torch.zeros(1, dtype=torch.int32, device=dev)
     need = lib.nvfp4_linear_workspace_bytes(M, N, 2 * kb)
     ws = _new1(need, torch.uint8, dev) if need else None
-    nvfp4_linear(*a, *b, ws, c, err_flag, stream)
+    _nvfp4_linear(a, b, ws, c, err_flag, stream)
     return c
 
 
@@ -489,9 +493,20 @@ def _entry(mode, name):
     return f"{mode}_{name}"
 
 
-def _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream):
-    dev = _device(entry, x, codes, scales, codes_t, scales_t, ts, err_flag)
+def _quantize_t(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream):
+    """Checks x, ts and err_flag (not the outputs' shapes) and calls entry."""
     ld = _rows(x, "x")
+    dev = _device(entry, x, codes, scales, codes_t, scales_t, ts, err_flag)
+    rows, cols = x.shape
+    _word(ts, "ts", torch.float32)
+    _word(err_flag, "err_flag", torch.int32)
+    _call(entry, dev, stream, x.data_ptr(), _dtype(x, "x"), rows, cols, ld, _at(codes),
+          _at(scales), codes_t.data_ptr(), scales_t.data_ptr(), ts.data_ptr(), ts_mode,
+          _at(err_flag))
+
+
+def _quantize_t_into(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream):
+    _rows(x, "x")
     rows, cols = x.shape
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales go together")
@@ -501,25 +516,21 @@ def _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, er
         _dense(scales, "scales", u8, (rows, cols // 16))
     _dense(codes_t, "codes_t", u8, (cols, rows // 2))
     _dense(scales_t, "scales_t", u8, (cols, rows // 16))
-    _word(ts, "ts", torch.float32)
-    _word(err_flag, "err_flag", torch.int32)
-    _call(entry, dev, stream, x.data_ptr(), _dtype(x, "x"), rows, cols, ld, _at(codes),
-          _at(scales), codes_t.data_ptr(), scales_t.data_ptr(), ts.data_ptr(), ts_mode,
-          _at(err_flag))
+    _quantize_t(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream)
 
 
 def if4_quantize_t(x, codes, scales, codes_t, scales_t, ts, ts_mode=TS_COMPUTE, err_flag=None,
                    stream=None):
     """IF4 of x^T (codes_t [cols, rows/2], scales_t [cols, rows/16]) and, when
     codes and scales are given, of x as well."""
-    _quantize_t_call("if4_quantize_t", x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag,
+    _quantize_t_into("if4_quantize_t", x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag,
                      stream)
 
 
 def nvfp4_quantize_t(x, codes, scales, codes_t, scales_t, ts, ts_mode=TS_COMPUTE, err_flag=None,
                      stream=None):
     """NVFP4 of x^T and, when codes and scales are given, of x as well."""
-    _quantize_t_call("nvfp4_quantize_t", x, codes, scales, codes_t, scales_t, ts, ts_mode,
+    _quantize_t_into("nvfp4_quantize_t", x, codes, scales, codes_t, scales_t, ts, ts_mode,
                      err_flag, stream)
 
 
@@ -529,7 +540,8 @@ def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=No
     codes_t, scales_t, ts) of x and of x^T under one tensor scale.  ts=None
     computes it; a float32 tensor is used as given."""
     entry = _entry(mode, "quantize_t")
-    _rows(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
     (rows, cols), dev, u8 = x.shape, x.device, torch.uint8
     codes_t, scales_t = _new(cols, rows // 2, u8, dev), _new(cols, rows // 16, u8, dev)
     codes = scales = None
@@ -539,7 +551,7 @@ def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=No
         ts, ts_mode = _new1(1, torch.float32, dev), TS_COMPUTE
     else:
         ts_mode = TS_GIVEN
-    _quantize_t_call(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream)
+    _quantize_t(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream)
     if with_rows:
         return codes, scales, codes_t, scales_t, ts
     return codes_t, scales_t, ts
@@ -552,18 +564,14 @@ def _norm_weight(weight, cols, dtype):
         raise ValueError(f"weight must be {dtype} or float32")
 
 
-def _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
-                   stream):
-    dev = _device(entry, x, residual, weight, h, rstd, codes, scales, ts, amax, err_flag)
+def _rms_norm(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag, stream):
+    """Checks the inputs (of the outputs only h) and calls entry."""
     ld, shape, dtype = _rows(x, "x"), x.shape, x.dtype
+    dev = _device(entry, x, residual, weight, h, rstd, codes, scales, ts, amax, err_flag)
     rows, cols = shape
     ld_res = 0 if residual is None else _rows(residual, "residual", dtype, shape)
     ld_h = 0 if h is None else _rows(h, "h", dtype, shape)
     _norm_weight(weight, cols, dtype)
-    _dense(codes, "codes", torch.uint8, (rows, cols // 2))
-    _dense(scales, "scales", torch.uint8, (rows, cols // 16))
-    if rstd is not None:
-        _dense(rstd, "rstd", torch.float32, (rows,))
     _word(ts, "ts", torch.float32)
     _word(amax, "amax", torch.float32)
     _word(err_flag, "err_flag", torch.int32)
@@ -572,18 +580,29 @@ def _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, 
           codes.data_ptr(), scales.data_ptr(), ts.data_ptr(), _at(amax), _at(err_flag))
 
 
+def _rms_norm_into(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
+                   stream):
+    _rows(x, "x")
+    rows, cols = x.shape
+    _dense(codes, "codes", torch.uint8, (rows, cols // 2))
+    _dense(scales, "scales", torch.uint8, (rows, cols // 16))
+    if rstd is not None:
+        _dense(rstd, "rstd", torch.float32, (rows,))
+    _rms_norm(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag, stream)
+
+
 def if4_rms_norm_quantize(x, residual, weight, eps, h, rstd, codes, scales, ts, amax=None,
                           err_flag=None, stream=None):
     """RMS norm of x (+ residual) quantized to IF4 under the given ts; residual,
     h, rstd and amax may be None."""
-    _rms_norm_call("if4_rms_norm_quantize", x, residual, weight, eps, h, rstd, codes, scales, ts,
+    _rms_norm_into("if4_rms_norm_quantize", x, residual, weight, eps, h, rstd, codes, scales, ts,
                    amax, err_flag, stream)
 
 
 def nvfp4_rms_norm_quantize(x, residual, weight, eps, h, rstd, codes, scales, ts, amax=None,
                             err_flag=None, stream=None):
     """RMS norm of x (+ residual) quantized to NVFP4 under the given ts."""
-    _rms_norm_call("nvfp4_rms_norm_quantize", x, residual, weight, eps, h, rstd, codes, scales, ts,
+    _rms_norm_into("nvfp4_rms_norm_quantize", x, residual, weight, eps, h, rstd, codes, scales, ts,
                    amax, err_flag, stream)
 
 
@@ -594,13 +613,13 @@ def rms_norm_quantize(x, weight, ts, residual=None, eps=1e-6, mode="if4", amax=N
     (x itself without a residual) and rstd [rows] are what rms_norm_backward
     takes.  amax: a float32 tensor raised to max |y|, for the next ts."""
     entry = _entry(mode, "rms_norm_quantize")
-    _rows(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
     (rows, cols), dev = x.shape, x.device
     codes, scales = _new(rows, cols // 2, torch.uint8, dev), _new(rows, cols // 16, torch.uint8, dev)
     rstd = _new1(rows, torch.float32, dev)
     h = None if residual is None else _new(rows, cols, x.dtype, dev)
-    _rms_norm_call(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
-                   stream)
+    _rms_norm(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag, stream)
     return codes, scales, x if h is None else h, rstd
 
 
@@ -619,9 +638,11 @@ def if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, workspace, str
     _norm_weight(weight, cols, dtype)
     _dense(rstd, "rstd", torch.float32, (rows,))
     _dense(dweight, "dweight", torch.float32, (cols,))
+    wp, wn = ((None, 0) if workspace is None else
+              (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     _call(name, dev, stream, dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(),
           _dtype(weight, "weight"), rstd.data_ptr(), _at(dres), ld_dres, _dtype(h, "h"), rows, cols,
-          dx.data_ptr(), ld_dx, dweight.data_ptr(), *_workspace(workspace))
+          dx.data_ptr(), ld_dx, dweight.data_ptr(), wp, wn)
 
 
 def rms_norm_backward(dy, h, weight, rstd, dres=None, stream=None):

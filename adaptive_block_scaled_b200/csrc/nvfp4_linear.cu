@@ -476,7 +476,8 @@ constexpr int OVERLAP = 2 * BN + SF_COLS - 512;   // 48
 constexpr int ACC1 = BN - OVERLAP;             // first column of the second accumulator
 constexpr int SF_COL0 = 512 - SF_COLS;
 constexpr int BAR_OFF = STAGES * STAGE;
-constexpr int SMEM = BAR_OFF + 256 + 1024;
+constexpr int OUT_OFF = BAR_OFF + 256;         // per epilogue warp: 32 x 33 words
+constexpr int SMEM = OUT_OFF + 4 * 32 * 33 * 4 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory");
 static_assert(ACC1 + BN <= SF_COL0 && OVERLAP == 48, "tensor memory");
 
@@ -541,16 +542,19 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
                  : "memory");
 }
 
-// N accumulator columns (16 or 32) of one row, scaled, to C's type.  width:
-// bytes that C's alignment and N allow per store (32, 16 or less)
+// COLS (16 or 32) accumulator columns of a warp's 32 rows (lane: row), scaled,
+// to C's type.  width: bytes that C's base and row length allow per store, 32
+// or 16; 0: elements only.  Then a lane's stores would touch a sector each for
+// two or four bytes, so the block goes through the warp's shared memory (rows
+// of 33 words) and leaves row by row, lanes along the columns.
 template <int ODT, int COLS>
-__device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float scale, int row, int M,
-                                           int N, int col0, int width)
+__device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float scale, int row0, int M,
+                                           int N, int col0, int width, uint32_t *stage)
 {
-    if (row >= M) return;
-    const int64_t base = (int64_t)row * N + col0;
+    const int lane = threadIdx.x & 31;
     constexpr int ES = ODT == IF4_F32 ? 4 : 2;
     if (width >= 16 && col0 + COLS <= N) {
+        if (row0 + lane >= M) return;
         uint32_t w[COLS * ES / 4];
 #pragma unroll
         for (int i = 0; i < COLS; i += 2) {
@@ -563,23 +567,28 @@ __device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float sca
                 w[i / 2] = ODT == IF4_BF16 ? bf16x2_from_f32(lo, hi) : f16x2_from_f32(lo, hi);
             }
         }
-        uint8_t *p = static_cast<uint8_t *>(c) + base * ES;
+        uint8_t *p = static_cast<uint8_t *>(c) + ((int64_t)(row0 + lane) * N + col0) * ES;
         if (width == 32) {
 #pragma unroll
-            for (int q = 0; q < COLS * ES / 32; ++q) {
-                const uint32_t(&x)[8] = *reinterpret_cast<const uint32_t(*)[8]>(w + 8 * q);
-                st_v8(p + 32 * q, x);
-            }
+            for (int q = 0; q < COLS * ES / 32; ++q)
+                st_v8(p + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(w + 8 * q));
         } else {
 #pragma unroll
             for (int q = 0; q < COLS * ES / 16; ++q)
                 st_v4(p + 16 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         }
     } else {
+        __syncwarp();                      // the previous block has been read
 #pragma unroll
-        for (int i = 0; i < COLS; ++i)
-            if (col0 + i < N)
-                store_c<ODT>(c, base + i, __fmul_rn(__uint_as_float(r[i]), scale));
+        for (int i = 0; i < COLS; ++i) stage[lane * 33 + i] = r[i];
+        __syncwarp();
+        // 32 / COLS rows at a time
+        const int col = lane % COLS, sub = lane / COLS;
+        const int rows = min(32, M - row0);
+        if (col0 + col < N)
+            for (int q = sub; q < rows; q += 32 / COLS)
+                store_c<ODT>(c, (int64_t)(row0 + q) * N + col0 + col,
+                             __fmul_rn(__uint_as_float(stage[q * 33 + col]), scale));
     }
 }
 
@@ -735,10 +744,11 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
         const uintptr_t al = reinterpret_cast<uintptr_t>(c) | (uintptr_t)((int64_t)N * ES);
         const int width = al % 32 == 0 ? 32 : al % 16 == 0 ? 16 : 0;
         const uint32_t free_bar = map_to(smem_u32(acc_free), 0);
+        uint32_t *stage = reinterpret_cast<uint32_t *>(smem + OUT_OFF) + quarter * (32 * 33);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int t = pair_id; t < tiles; t += num_pairs) {
-            const int row = (t % m_tiles) * 2 * PM + (int)rank * PM + quarter * 32 + lane;
+            const int row0 = (t % m_tiles) * 2 * PM + (int)rank * PM + quarter * 32;
             const int n0 = (t / m_tiles) * BN;
             if (!warp_wait(smem_u32(&acc_full[acc]), acc_phase, abort_flag)) break;
             tc_fence_after();
@@ -753,16 +763,17 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(free_bar);
-            store_cols<ODT, 32>(c, r, scale, row, M, N, n0 + c0, width);
-            store_cols<ODT, 16>(c, q, scale, row, M, N, n0 + c0 + 32, width);
+            store_cols<ODT, 32>(c, r, scale, row0, M, N, n0 + c0, width, stage);
+            store_cols<ODT, 16>(c, q, scale, row0, M, N, n0 + c0 + 32, width, stage);
             const uint32_t base = lanes + (uint32_t)(acc * ACC1 + rest);
 #pragma unroll 1
             for (int ch = 0; ch < ACC1 / 32; ++ch) {
                 tmem_ld32(base + ch * 32, r);
-                store_cols<ODT, 32>(c, r, scale, row, M, N, n0 + rest + ch * 32, width);
+                store_cols<ODT, 32>(c, r, scale, row0, M, N, n0 + rest + ch * 32, width, stage);
             }
             tmem_ld16(base + ACC1 / 32 * 32, q);
-            store_cols<ODT, 16>(c, q, scale, row, M, N, n0 + rest + ACC1 / 32 * 32, width);
+            store_cols<ODT, 16>(c, q, scale, row0, M, N, n0 + rest + ACC1 / 32 * 32, width,
+                                stage);
             acc_phase ^= (uint32_t)acc;
             acc ^= 1;
         }
