@@ -176,17 +176,19 @@ constexpr int THREADS = 192;                   // TMA, MMA, four scale / epilogu
 constexpr int SF_UNITS = 3;
 constexpr int SF_UNIT_BYTES = 4 * SF_BLOCK;    // two stages x (weights, tokens)
 constexpr int SF_COLS = 2 * 2 * KSTEPS * 4;    // two stages of scale columns
+constexpr int MAX_RANKS = 8;                   // the portable cluster size
 
 template <int NT>
 struct Cfg {
     static constexpr int X_BYTES = NT * SK / 2;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    // up to 32 tokens: two CTAs of 106-116 KB per SM; above: one per SM
-    static constexpr int STAGES = NT <= 16 ? 4 : NT <= 32 ? 4 : NT <= 64 ? 7 : 6;
+    static constexpr int PER_SM = NT <= 32 ? 2 : 1;      // CTAs per SM: 97-105 or 193 KB each
+    static constexpr int STAGES = NT <= 32 ? 4 : 7;
     static constexpr int SF_OFF = STAGES * STAGE;
     static constexpr int BAR_OFF = SF_OFF + SF_UNITS * SF_UNIT_BYTES;
     static constexpr int SMEM = BAR_OFF + 256 + 1024;
-    static constexpr int TMEM_COLS = NT + SF_COLS <= 128 ? 128 : 256;
+    static constexpr int TMEM_COLS = 128;
+    static_assert(NT + SF_COLS <= TMEM_COLS, "tensor memory");
     static_assert(NT * WR * 4 <= SF_OFF, "the partial tile fits the stages");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -223,7 +225,7 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
     const uint32_t rank = cta_rank();
     const int n0 = blockIdx.y * WR;
-    const int m0 = blockIdx.z * NT;
+    const int m0 = (int)(blockIdx.x / ranks) * NT;
     const int units = (K + UNIT - 1) / UNIT;
     const int u0 = (int)((int64_t)units * rank / ranks);
     const int u1 = (int)((int64_t)units * (rank + 1) / ranks);
@@ -409,22 +411,34 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
     __syncthreads();
     if (ranks > 1) {
         cluster_sync();
-        if (warp >= 2 && !*abort_flag) {
-            const int row = (warp & 3) * 32 + lane;
+        // rank r adds tokens r, r + ranks, ...: a warp per token, four rows per
+        // lane, the partials of all ranks loaded before they are added in order
+        if (!*abort_flag) {
             const float scale = __fmul_rn(*x_ts, *w_ts);
-            const uint32_t part = smem_u32(smem);
-            if (n0 + row < N)
-                for (int m = rank; m < NT && m0 + m < M; m += ranks) {
-                    float sum = 0.0f;
-                    for (uint32_t s = 0; s < ranks; ++s) {
-                        float v;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(v) : "r"(map_to(part + (m * WR + row) * 4, s))
-                                     : "memory");
-                        sum = __fadd_rn(sum, v);
-                    }
-                    store_c<ODT>(c, (int64_t)(m0 + m) * N + n0 + row, __fmul_rn(sum, scale));
+            uint32_t part[MAX_RANKS];
+#pragma unroll
+            for (uint32_t s = 0; s < MAX_RANKS; ++s)
+                part[s] = map_to(smem_u32(smem) + lane * 16, s < ranks ? s : 0);
+            const int n = n0 + 4 * lane;
+            const int tokens = min(NT, M - m0);
+            for (int m = (int)rank + (int)ranks * warp; m < tokens; m += (int)ranks * (THREADS / 32)) {
+                float v[MAX_RANKS][4];
+#pragma unroll
+                for (uint32_t s = 0; s < MAX_RANKS; ++s)
+                    if (s < ranks)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(v[s][0]), "=f"(v[s][1]), "=f"(v[s][2]), "=f"(v[s][3])
+                                     : "r"(part[s] + m * WR * 4) : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float sum = v[0][i];
+#pragma unroll
+                    for (uint32_t s = 1; s < MAX_RANKS; ++s)
+                        if (s < ranks) sum = __fadd_rn(sum, v[s][i]);
+                    if (n + i < N)
+                        store_c<ODT>(c, (int64_t)(m0 + m) * N + n + i, __fmul_rn(sum, scale));
                 }
+            }
         }
         cluster_sync();                  // no CTA leaves while another reads its partials
     }
@@ -439,12 +453,12 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
 
 // --------------------------------------------------- many rows: CTA pairs ----
 //
-// A pair of CTAs on two SMs computes 256 x 256 tiles with tcgen05.mma of
+// A pair of CTAs on two SMs computes 256 x BN tiles with tcgen05.mma of
 // cta_group::2, persistent over the tiles: CTA r holds rows r * 128..+127 of
 // A's slab and half of B's, the leader's MMAs read both halves, and each CTA
 // keeps its own 128 rows of the product.  The MMA reads a row's scales from
 // the tensor memory of the CTA that holds the accumulator, so each CTA brings
-// the scales of its own A rows and of all 256 B rows.
+// the scales of its own A rows and of all BN rows of B.
 //
 // Scales: a small kernel first puts both operands' scales into the workspace
 // in the order that tcgen05.cp reads (pack_scales), so that here they are two
@@ -453,42 +467,58 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
 // 4096: 135 us, the ring's round trips and the loads' latency in the way of
 // every stage.
 //
-// Tensor memory: two accumulators of 256 columns and the scales' 48 do not fit
-// 512 columns, and narrower tiles read A's shared memory more often per
-// column: without stores 40.9 us for 256 columns, 49.5 for 224, 56.0 for 192.
-// So the accumulators overlap in OVERLAP columns: the epilogue first takes the
-// overlap to registers and releases it, and the next tile's MMAs run under the
-// rest.
+// Tensor memory: two accumulators of BN columns, so that the epilogue of one
+// tile runs under the MMAs of the next, and the scale columns of two K steps:
+// 2 * 240 + 32 = 512.  (256 columns with the accumulators overlapping, the
+// overlap drained first: the wait for it cost 0.6 us a tile, and over the
+// sizes tried it was 5 % faster to 9 % slower.)  A wide tile reads less shared memory
+// per product; narrow ones use more SMs when there are few tiles.  Measured, BN =
+// 240 against 128, us: 8192 x 4096 x 4096 68.6 / 86.5, 1024 x 4096 x 4096
+// 12.7 / 15.8 (72 and 128 tiles), 512 x 4096 x 4096 11.9 / 11.5 (36 and 64),
+// 1001 x 1555 x 4128 22.0 / 16.6 (28 and 52): 128 while its tiles fit the pairs.
+//
+// Long runs are bound by the board's power: 8192 x 4096 x 4096 takes 58 us in
+// bursts and 69 us when repeated for 0.1 s.
 
 namespace duo {
 
 constexpr int PM = 128;                        // rows per CTA
-constexpr int BN = 256;                        // columns per pair
 constexpr int A_BYTES = PM * SK / 2;           // 16 KB per stage
-constexpr int B_BYTES = BN / 2 * SK / 2;       // 16 KB
 constexpr int SFA_BYTES = SF_BLOCK;            // 2 KB
-constexpr int SFB_BYTES = 2 * SF_BLOCK;        // 4 KB: two blocks of 128 rows
-constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-constexpr int STAGES = 5;
 constexpr int THREADS = 192;                   // TMA, MMA, 4 epilogue warps
-constexpr int SF_COLS = 3 * KSTEPS * 4;        // scale columns of a stage
-constexpr int OVERLAP = 2 * BN + SF_COLS - 512;   // 48
-constexpr int ACC1 = BN - OVERLAP;             // first column of the second accumulator
-constexpr int SF_COL0 = 512 - SF_COLS;
-constexpr int BAR_OFF = STAGES * STAGE;
-constexpr int OUT_OFF = BAR_OFF + 256;         // per epilogue warp: 32 x 33 words
-constexpr int SMEM = OUT_OFF + 4 * 32 * 33 * 4 + 1024;
-static_assert(SMEM <= 227 * 1024, "shared memory");
-static_assert(ACC1 + BN <= SF_COL0 && OVERLAP == 48, "tensor memory");
+constexpr int OUT_BYTES = 4608;                // staged output per epilogue warp
+constexpr int OUT_BOX = 32 * 64;               // 32 rows x 32 two-byte columns, two buffers
+
+template <int BN>
+struct Cfg {
+    static constexpr int B_BYTES = BN / 2 * SK / 2;
+    static constexpr int SFB_BLOCKS = (BN + 127) / 128;
+    static constexpr int SFB_BYTES = SFB_BLOCKS * SF_BLOCK;
+    static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+    static constexpr int STAGES = BN > 128 ? 5 : 7;
+    static constexpr int SF_STEP_COLS = 4 + 4 * SFB_BLOCKS;      // scale columns of a K step
+    static constexpr int SF_COL0 = 512 - 32;                     // two K steps in turn
+    static constexpr int OUT_OFF = STAGES * STAGE;
+    static constexpr int BAR_OFF = OUT_OFF + 4 * OUT_BYTES;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(2 * BN <= SF_COL0 && SF_STEP_COLS <= 16, "tensor memory");
+    static_assert(BN % 16 == 0 && STAGE % 1024 == 0 && B_BYTES % 1024 == 0, "alignment");
+};
 
 }  // namespace duo
 
-// The scales of one operand: [rows, K / 16] as stored, and [row blocks of 128]
-// [K steps of 64, a multiple of 4][512 bytes] as tcgen05.cp reads them.
+// The scales of one operand: [rows, K / 16] as stored, and [tiles of `tile`
+// rows][`blocks` blocks of 128][K steps of 64, a multiple of 4][512 bytes] as
+// tcgen05.cp reads them; rows past a tile's end are 0.
 struct ScalePack {
     const uint8_t *src;
     uint8_t *dst;
-    int rows;
+    int rows, tile, blocks;
+    __host__ __device__ int64_t row_blocks() const
+    {
+        return (int64_t)((rows + tile - 1) / tile) * blocks;
+    }
 };
 
 // A thread takes one stage (four K steps) of the rows m, m + 32, m + 64 and
@@ -501,8 +531,8 @@ pack_scales(ScalePack a, ScalePack b, int K, int *err)
 {
     pdl_enter();
     const int kg = K / 16, stages = (K + SK - 1) / SK, pairs = (stages + 1) / 2;
-    const int64_t na = (int64_t)((a.rows + 127) / 128) * pairs * 2;   // warps' work items
-    const int64_t nb = (int64_t)((b.rows + 127) / 128) * pairs * 2;
+    const int64_t na = a.row_blocks() * pairs * 2;           // warps' work items
+    const int64_t nb = b.row_blocks() * pairs * 2;
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0;
     for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < na + nb;
@@ -510,22 +540,27 @@ pack_scales(ScalePack a, ScalePack b, int K, int *err)
         const bool first = w < na;
         const uint8_t *src = first ? a.src : b.src;
         uint8_t *dst = first ? a.dst : b.dst;
-        const int rows = first ? a.rows : b.rows;
-        const int64_t i = first ? w : w - na;
+        const int rows = first ? a.rows : b.rows, tile_rows = first ? a.tile : b.tile;
+        const int blocks = first ? a.blocks : b.blocks;
+        // (row blocks x stages fit 32 bits: 2^15 blocks of rows, 2^12 stages)
+        const uint32_t i = (uint32_t)(first ? w : w - na);
         const int m = (int)(i & 1) * 16 + (lane >> 1);
-        const int64_t pr = i >> 1;
-        const int stage = (int)(pr % pairs) * 2 + (lane & 1);
-        const int64_t block = pr / pairs;
+        const uint32_t block = (i >> 1) / (uint32_t)pairs;
+        const int stage = (int)((i >> 1) - block * (uint32_t)pairs) * 2 + (lane & 1);
         if (stage >= stages) continue;
+        const uint32_t tile = block / (uint32_t)blocks;
+        const int in_tile0 = (int)(block - tile * (uint32_t)blocks) * 128;
         uint32_t v[4][4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const int64_t row = block * 128 + m + 32 * p;
-            load_scales16<VEC>(src + row * kg + stage * 16, row < rows ? kg - stage * 16 : 0, v[p]);
+            const int in_tile = in_tile0 + m + 32 * p;
+            const int64_t row = (int64_t)tile * tile_rows + in_tile;
+            load_scales16<VEC>(src + row * kg + stage * 16,
+                               in_tile < tile_rows && row < rows ? kg - stage * 16 : 0, v[p]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) bad |= v[p][j];
         }
-        uint8_t *d = dst + ((block * stages + stage) * KSTEPS) * SF_STEP + m * 16;
+        uint8_t *d = dst + ((int64_t)block * stages + stage) * SF_BLOCK + m * 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j) st_v4(d + j * SF_STEP, v[0][j], v[1][j], v[2][j], v[3][j]);
     }
@@ -592,16 +627,57 @@ __device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float sca
     }
 }
 
+// The same for two-byte C whose rows are multiples of 16 bytes, 32 whole
+// columns: through shared memory (64-byte rows, swizzled as the tensor map
+// says) and a TMA store, which writes whole lines and clips at C's edges
+// (direct 32-byte stores of a row per lane: 16384 x 8192 x 8192 553 against
+// 524 us, 512 x 4096 x 4096 12.4 against 11.9 us).
 template <int ODT>
+__device__ __forceinline__ void store_box(const CUtensorMap *map, const uint32_t *r, float scale,
+                                          int row0, int col0, uint32_t buf)
+{
+    const int lane = threadIdx.x & 31;
+    // the store two boxes ago has read this buffer
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float lo = __fmul_rn(__uint_as_float(r[8 * q + 2 * i]), scale);
+            const float hi = __fmul_rn(__uint_as_float(r[8 * q + 2 * i + 1]), scale);
+            w[i] = ODT == IF4_BF16 ? bf16x2_from_f32(lo, hi) : f16x2_from_f32(lo, hi);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                     :: "r"(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)), "r"(w[0]), "r"(w[1]),
+                        "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                     :: "l"(reinterpret_cast<uint64_t>(map)), "r"(col0), "r"(row0), "r"(buf)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+template <int BN, int ODT>
 __global__ void __launch_bounds__(duo::THREADS, 1)
 nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
                   const __grid_constant__ CUtensorMap tmap_b,
                   const __grid_constant__ CUtensorMap tmap_sa,
                   const __grid_constant__ CUtensorMap tmap_sb,
+                  const __grid_constant__ CUtensorMap tmap_c, int box_stores,
                   const float *__restrict__ a_ts, const float *__restrict__ b_ts,
                   void *__restrict__ c, int M, int N, int K, int *err)
 {
     using namespace duo;
+    using C = Cfg<BN>;
+    constexpr int STAGES = C::STAGES, STAGE = C::STAGE, B_BYTES = C::B_BYTES;
+    constexpr int SFB_BYTES = C::SFB_BYTES, SFB_BLOCKS = C::SFB_BLOCKS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -609,11 +685,11 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
     uint8_t *smem_b = smem_a + STAGES * A_BYTES;
     uint8_t *smem_sa = smem_b + STAGES * B_BYTES;
     uint8_t *smem_sb = smem_sa + STAGES * SFA_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + BAR_OFF);   // leader
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);   // leader
     uint64_t *empty = full + STAGES;               // both
     uint64_t *acc_full = empty + STAGES;           // both
-    uint64_t *acc_free = acc_full + 2;             // leader: the overlap is free
-    uint64_t *drain = acc_free + 1;                // leader
+    uint64_t *acc_free = acc_full + 2;             // leader, [2]
+    uint64_t *drain = acc_free + 2;                // leader
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -634,7 +710,8 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
         }
         mbar_init(smem_u32(&acc_full[0]), 1);
         mbar_init(smem_u32(&acc_full[1]), 1);
-        mbar_init(smem_u32(acc_free), 2 * 4);
+        mbar_init(smem_u32(&acc_free[0]), 2 * 4);
+        mbar_init(smem_u32(&acc_free[1]), 2 * 4);
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -642,6 +719,7 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
         prefetch_tmap(&tmap_b);
         prefetch_tmap(&tmap_sa);
         prefetch_tmap(&tmap_sb);
+        if (box_stores) prefetch_tmap(&tmap_c);
     }
     if (warp == 1) {
         __syncwarp();
@@ -675,7 +753,7 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
                 tma_load_3d_pair(smem_u32(smem_sa + stage * SFA_BYTES), &tmap_sa, 0, kb * KSTEPS,
                                  mt * 2 + (int)rank, fb);
                 tma_load_3d_pair(smem_u32(smem_sb + stage * SFB_BYTES), &tmap_sb, 0, kb * KSTEPS,
-                                 nt * 2, fb);
+                                 nt * SFB_BLOCKS, fb);
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
@@ -691,16 +769,16 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
         const uint64_t b_desc = smem_desc_sw128(smem_u32(smem_b));
         const uint64_t sa_desc = smem_desc_scales(smem_u32(smem_sa));
         const uint64_t sb_desc = smem_desc_scales(smem_u32(smem_sb));
-        const uint32_t ta0 = tmem_base + SF_COL0, tb0 = ta0 + KSTEPS * 4;
+        const uint32_t sf_tmem = tmem_base + C::SF_COL0;
         int stage = 0, acc = 0;
         uint32_t phase = 0, free_phase = 1;
         bool ok = true;
         for (int t = pair_id; t < tiles && ok; t += num_pairs) {
-            // the previous tile's epilogue holds the overlap until it says so
-            if (!warp_wait<true>(smem_u32(acc_free), free_phase, abort_flag)) break;
-            free_phase ^= 1u;
+            // the epilogue of two tiles ago has drained this accumulator
+            if (!warp_wait<true>(smem_u32(&acc_free[acc]), free_phase, abort_flag)) break;
+            free_phase ^= (uint32_t)acc;
             tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC1);
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
             for (int kb = 0; kb < k_blocks; ++kb) {
                 if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag)) { ok = false; break; }
                 tc_fence_after();
@@ -713,10 +791,11 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                     for (int kk = 0; kk < KSTEPS; ++kk) {
                         if (kk < steps) {
-                            const uint32_t ta = ta0 + kk * 4, tb = tb0 + kk * 8;
+                            const uint32_t ta = sf_tmem + (kk & 1) * 16, tb = ta + 4;
                             copy_scales<2>(ta, sad + kk * (SF_STEP >> 4));
-                            copy_scales<2>(tb, sbd + kk * (SF_STEP >> 4));
-                            copy_scales<2>(tb + 4, sbd + ((SF_BLOCK + kk * SF_STEP) >> 4));
+#pragma unroll
+                            for (int j = 0; j < SFB_BLOCKS; ++j)
+                                copy_scales<2>(tb + 4 * j, sbd + ((j * SF_BLOCK + kk * SF_STEP) >> 4));
                             umma_nvfp4<2>(d_tmem, ad + 2 * kk, bd + 2 * kk, mxf4_idesc(2 * PM, BN),
                                           ta, tb, (kb | kk) != 0 ? 1u : 0u);
                         }
@@ -743,8 +822,11 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
         constexpr int ES = ODT == IF4_F32 ? 4 : 2;
         const uintptr_t al = reinterpret_cast<uintptr_t>(c) | (uintptr_t)((int64_t)N * ES);
         const int width = al % 32 == 0 ? 32 : al % 16 == 0 ? 16 : 0;
-        const uint32_t free_bar = map_to(smem_u32(acc_free), 0);
-        uint32_t *stage = reinterpret_cast<uint32_t *>(smem + OUT_OFF) + quarter * (32 * 33);
+        const uint32_t free_bar[2] = {map_to(smem_u32(&acc_free[0]), 0),
+                                      map_to(smem_u32(&acc_free[1]), 0)};
+        uint32_t *stage = reinterpret_cast<uint32_t *>(smem + C::OUT_OFF + quarter * OUT_BYTES);
+        const uint32_t boxes = smem_u32(stage);
+        int box = 0;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int t = pair_id; t < tiles; t += num_pairs) {
@@ -753,30 +835,42 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
             if (!warp_wait(smem_u32(&acc_full[acc]), acc_phase, abort_flag)) break;
             tc_fence_after();
             const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
-            // the overlap: the first accumulator's last 48 columns, the
-            // second's first 48
-            const int c0 = acc ? 0 : ACC1;
-            const int rest = acc ? OVERLAP : 0;
-            uint32_t r[32], q[16];
-            tmem_ld32(lanes + ACC1, r);
-            tmem_ld16(lanes + ACC1 + 32, q);
+            auto put32 = [&](const uint32_t (&r)[32], int col) {
+                if (ODT != IF4_F32 && box_stores) {
+                    if (row0 < M && n0 + col < N) {
+                        store_box<ODT>(&tmap_c, r, scale, row0, n0 + col, boxes + box * OUT_BOX);
+                        box ^= 1;          // only a box that was stored takes a buffer
+                    }
+                } else {
+                    store_cols<ODT, 32>(c, r, scale, row0, M, N, n0 + col, width, stage);
+                }
+            };
+            const uint32_t base = lanes + (uint32_t)(acc * BN);
+#pragma unroll 1
+            for (int ch = 0; ch < BN / 32; ++ch) {
+                uint32_t r[32];
+                tmem_ld32(base + ch * 32, r);
+                put32(r, ch * 32);
+            }
+            if constexpr (BN % 32 != 0) {
+                uint32_t q[16];
+                tmem_ld16(base + BN / 32 * 32, q);
+                const int col = n0 + BN / 32 * 32;
+                // element stores at C's edge go through the boxes' memory
+                if (box_stores && col + 16 > N) {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+                }
+                store_cols<ODT, 16>(c, q, scale, row0, M, N, col, width, stage);
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_remote(free_bar);
-            store_cols<ODT, 32>(c, r, scale, row0, M, N, n0 + c0, width, stage);
-            store_cols<ODT, 16>(c, q, scale, row0, M, N, n0 + c0 + 32, width, stage);
-            const uint32_t base = lanes + (uint32_t)(acc * ACC1 + rest);
-#pragma unroll 1
-            for (int ch = 0; ch < ACC1 / 32; ++ch) {
-                tmem_ld32(base + ch * 32, r);
-                store_cols<ODT, 32>(c, r, scale, row0, M, N, n0 + rest + ch * 32, width, stage);
-            }
-            tmem_ld16(base + ACC1 / 32 * 32, q);
-            store_cols<ODT, 16>(c, q, scale, row0, M, N, n0 + rest + ACC1 / 32 * 32, width,
-                                stage);
+            if (lane == 0) arrive_remote(free_bar[acc]);
             acc_phase ^= (uint32_t)acc;
             acc ^= 1;
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -844,8 +938,9 @@ int launch_split(const Problem &p, const DeviceInfo &d, int ranks)
         !make_codes_map(&mx, p.a_codes, p.M, p.K, NT))
         return IF4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)((p.N + split::WR - 1) / split::WR),
-                       (unsigned)((p.M + NT - 1) / NT));
+    // token tiles next to each other, so that they share a weight tile in L2
+    cfg.gridDim = dim3((unsigned)(ranks * ((p.M + NT - 1) / NT)),
+                       (unsigned)((p.N + split::WR - 1) / split::WR), 1);
     cfg.blockDim = dim3(split::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = p.st;
@@ -864,14 +959,28 @@ int launch_split(const Problem &p, const DeviceInfo &d, int ranks)
     return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
 }
 
+// Two-byte C [M, N] -> tensor map with a box of 32 columns x 32 rows.
+bool make_out_map(CUtensorMap *map, void *c, int64_t M, int64_t N)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    const cuuint64_t strides[1] = {(cuuint64_t)N * 2};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, c, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Packed scales [row blocks][K steps][512 bytes] -> tensor map with a box of
 // one stage (4 K steps) x `blocks` row blocks.
-bool make_scales_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int blocks)
+bool make_scales_map(CUtensorMap *map, const void *base, int64_t row_blocks, int64_t K, int blocks)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t steps = (cuuint64_t)((K + SK - 1) / SK) * KSTEPS;
-    const cuuint64_t dims[3] = {SF_STEP / 4, steps, (cuuint64_t)((rows + 127) / 128)};
+    const cuuint64_t dims[3] = {SF_STEP / 4, steps, (cuuint64_t)row_blocks};
     const cuuint64_t strides[2] = {SF_STEP, steps * SF_STEP};
     const cuuint32_t box[3] = {SF_STEP / 4, KSTEPS, (cuuint32_t)blocks};
     const cuuint32_t estr[3] = {1, 1, 1};
@@ -880,28 +989,35 @@ bool make_scales_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t packed_bytes(int64_t rows, int64_t K)
+// Bytes of one operand's packed scales (row blocks of 128).
+size_t packed_bytes(int64_t row_blocks, int64_t K)
 {
-    return (size_t)((rows + 127) / 128) * (size_t)((K + SK - 1) / SK) * SF_BLOCK;
+    return (size_t)row_blocks * (size_t)((K + SK - 1) / SK) * SF_BLOCK;
 }
 
 // The pair kernel takes problems above 128 rows and columns.
 bool use_pair(int64_t M, int64_t N) { return M > 128 && N > 128; }
 
-template <int VEC, int ODT>
+template <int BN, int VEC, int ODT>
 int launch_pair(const Problem &p, const DeviceInfo &d)
 {
-    auto kernel = nvfp4_linear_pair<ODT>;
+    using C = duo::Cfg<BN>;
+    auto kernel = nvfp4_linear_pair<BN, ODT>;
     static std::once_flag once[MAX_DEVICES], occ_once[MAX_DEVICES];
     static cudaError_t rcs[MAX_DEVICES];
     static int resident[MAX_DEVICES];
-    const int rc = allow_smem(kernel, duo::SMEM, d, once, rcs);
+    const int rc = allow_smem(kernel, C::SMEM, d, once, rcs);
     if (rc != IF4_OK) return rc;
-    uint8_t *wa = static_cast<uint8_t *>(p.workspace), *wb = wa + packed_bytes(p.M, p.K);
-    CUtensorMap ma, mb, msa, msb;
+    ScalePack sa{p.a_scales, static_cast<uint8_t *>(p.workspace), (int)p.M, 2 * duo::PM, 2};
+    ScalePack sb{p.b_scales, nullptr, (int)p.N, BN, C::SFB_BLOCKS};
+    sb.dst = sa.dst + packed_bytes(sa.row_blocks(), p.K);
+    const bool boxes = ODT != IF4_F32 && p.N % 8 == 0 && reinterpret_cast<uintptr_t>(p.c) % 16 == 0;
+    CUtensorMap ma, mb, msa, msb, mc = {};
     if (!make_codes_map(&ma, p.a_codes, p.M, p.K, duo::PM) ||
-        !make_codes_map(&mb, p.b_codes, p.N, p.K, duo::BN / 2) ||
-        !make_scales_map(&msa, wa, p.M, p.K, 1) || !make_scales_map(&msb, wb, p.N, p.K, 2))
+        !make_codes_map(&mb, p.b_codes, p.N, p.K, BN / 2) ||
+        !make_scales_map(&msa, sa.dst, sa.row_blocks(), p.K, 1) ||
+        !make_scales_map(&msb, sb.dst, sb.row_blocks(), p.K, C::SFB_BLOCKS) ||
+        (boxes && !make_out_map(&mc, p.c, p.M, p.N)))
         return IF4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = p.st;
@@ -910,17 +1026,16 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int64_t warps = ((p.M + 127) / 128 + (p.N + 127) / 128) * ((p.K + UNIT - 1) / UNIT) * 2;
+    const int64_t warps = (sa.row_blocks() + sb.row_blocks()) * ((p.K + UNIT - 1) / UNIT) * 2;
     const int64_t blocks = (warps + 7) / 8, most = (int64_t)d.sm_count * 8;
     cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
-    const ScalePack sa{p.a_scales, wa, (int)p.M}, sb{p.b_scales, wb, (int)p.N};
     if (cudaLaunchKernelEx(&cfg, pack_scales<VEC>, sa, sb, (int)p.K, p.err) != cudaSuccess)
         return IF4_ERR_CUDA;
 
     cfg.gridDim = dim3((unsigned)(2 * (d.sm_count / 2)), 1, 1);
     cfg.blockDim = dim3(duo::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = duo::SMEM;
+    cfg.dynamicSmemBytes = C::SMEM;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
@@ -935,12 +1050,12 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
         else
             (void)cudaGetLastError();
     });
-    const int64_t tiles = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + duo::BN - 1) / duo::BN);
+    const int64_t tiles = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + BN - 1) / BN);
     int64_t pairs = resident[d.id] > 0 ? resident[d.id] : d.sm_count / 2;
     if (pairs > d.sm_count / 2) pairs = d.sm_count / 2;
     if (tiles < pairs) pairs = tiles;
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, p.a_ts, p.b_ts, p.c, (int)p.M, (int)p.N,
+    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mc, boxes ? 1 : 0, p.a_ts, p.b_ts, p.c, (int)p.M, (int)p.N,
                            (int)p.K, p.err) != cudaSuccess)
         return IF4_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
@@ -949,18 +1064,32 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
 template <int VEC, int ODT>
 int launch_linear(const Problem &p, const DeviceInfo &d)
 {
-    if (use_pair(p.M, p.N)) return launch_pair<VEC, ODT>(p, d);
-    const int64_t units = (p.K + UNIT - 1) / UNIT;
-    auto ranks_for = [&](int64_t tiles) {
-        int s = 1;
-        while (s < 8 && 2 * s <= units && tiles * s < d.sm_count * 3 / 4) s *= 2;
-        return s;
-    };
+    if (use_pair(p.M, p.N)) {
+        // narrow tiles while each has a pair of SMs of its own
+        const int64_t narrow = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + 127) / 128);
+        return narrow <= d.sm_count / 2 ? launch_pair<128, VEC, ODT>(p, d)
+                                        : launch_pair<240, VEC, ODT>(p, d);
+    }
+    // As few tokens per CTA as leave each output tile an SM of its own (32
+    // tokens of 4096 x 4096: 16 per CTA 6.5 us, 32 per CTA 7.2), and the
+    // largest power of two of K ranks that still runs in one wave (a second
+    // wave costs more than all the splitting gains: 32 x 4096 x 4096 6.5 against
+    // 11.4 us).
     const int64_t wt = (p.N + split::WR - 1) / split::WR;
-    if (p.M <= 16) return launch_split<16, VEC, ODT>(p, d, ranks_for(wt));
-    if (p.M <= 32) return launch_split<32, VEC, ODT>(p, d, ranks_for(wt));
-    if (p.M <= 64) return launch_split<64, VEC, ODT>(p, d, ranks_for(wt));
-    return launch_split<128, VEC, ODT>(p, d, ranks_for(wt * ((p.M + 127) / 128)));
+    const int64_t units = (p.K + UNIT - 1) / UNIT;
+    auto run = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        const int64_t tiles = wt * ((p.M + NT - 1) / NT);
+        const int64_t slots = (int64_t)d.sm_count * split::Cfg<NT>::PER_SM;
+        int s = 1;
+        while (s < split::MAX_RANKS && 2 * s <= units && tiles * 2 * s <= slots) s *= 2;
+        return launch_split<NT, VEC, ODT>(p, d, s);
+    };
+    if (p.M <= 16 || wt * ((p.M + 15) / 16) <= d.sm_count)
+        return run(std::integral_constant<int, 16>{});
+    if (p.M <= 32 || wt * ((p.M + 31) / 32) <= d.sm_count)
+        return run(std::integral_constant<int, 32>{});
+    return run(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
@@ -968,7 +1097,8 @@ int launch_linear(const Problem &p, const DeviceInfo &d)
 extern "C" size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > MAX_MN || N > MAX_MN || K > MAX_K) return 0;
-    return use_pair(M, N) ? packed_bytes(M, K) + packed_bytes(N, K) : 0;
+    // the narrowest tile width needs the most blocks
+    return use_pair(M, N) ? packed_bytes((M + 255) / 256 * 2 + (N + 239) / 240 * 2, K) : 0;
 }
 
 extern "C" int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, const float *a_ts,

@@ -62,8 +62,9 @@ def test_linear_empty_is_ok(lib):
 def test_linear_workspace(lib):
     f = lib.nvfp4_linear_workspace_bytes
     assert f(1, 4096, 4096) == 0 and f(4096, 16, 64) == 0     # few rows, few columns
-    assert f(256, 512, 256) == (2 + 4) * 2048                 # 128 rows x 16 scales
-    assert f(257, 512, 288) == (3 + 4) * 2 * 2048             # rows and K rounded up
+    # blocks of 128 rows x 16 scales: two per 256 rows of A, two per 240 of B
+    assert f(256, 480, 256) == (2 + 4) * 2048
+    assert f(257, 481, 288) == (4 + 6) * 2 * 2048             # rows and K rounded up
     for bad in ((0, 4, 64), (4, 0, 64), (4, 4, 16), (4, 4, 40), (1 << 23, 4, 64)):
         assert f(*bad) == 0
 
