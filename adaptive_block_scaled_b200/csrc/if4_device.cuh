@@ -277,6 +277,17 @@ __device__ __forceinline__ void pdl_release()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A float that an earlier kernel of the stream may have written.  Read this
+// way it stays behind pdl_enter(): the compiler takes a load through a const
+// __restrict__ pointer for one of memory that never changes, and may move it
+// in front of the wait.
+__device__ __forceinline__ float ld_after_wait(const float *p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Wall clock in nanoseconds, for bounded waits.
 __device__ __forceinline__ unsigned long long globaltimer_ns()
 {

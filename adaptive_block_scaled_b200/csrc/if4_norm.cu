@@ -21,6 +21,9 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "../../include/if4.h"
 #include "if4_device.cuh"
@@ -113,6 +116,23 @@ struct NormArgs {
     double inv_cols, eps;
 };
 
+// s + v * v in binary64 for a binary32 value's bits.  The conversion instruction
+// runs at a quarter of the rate of the multiply-add beside it, so the value is
+// rebiased by hand: |v|'s bits moved down by 3 plus 896 exponents.  That takes
+// 0 and subnormals for numbers of about 2^-127, whose squares vanish beside
+// any eps, and Inf and NaN for finite ones, which the codes' check reports.
+// Values of 16-bit types leave the low word empty.
+template <int DT>
+__device__ __forceinline__ double add_square(double s, float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    uint32_t hi;
+    asm("mad.hi.u32 %0, %1, %2, %3;"
+        : "=r"(hi) : "r"(b & 0x7FFFFFFFu), "r"(0x20000000u), "r"(0x38000000u));
+    const double x = __hiloint2double((int)hi, DT == DT_F32 ? (int)(b << 29) : 0);
+    return fma(x, x, s);
+}
+
 // rstd of a row from its binary64 sum of squares.  The binary32 reciprocal root
 // (2^-22 off at most) and two Newton steps in binary64 leave 2^-52, so the one
 // rounding to binary32 is the rounding of the definition's value (which has
@@ -176,21 +196,114 @@ __device__ __forceinline__ void load_weight(const char *w, int g, Raw<WT> &r)
     const char *p = w + (int64_t)g * 16 * elem_bytes<WT>();
 #pragma unroll
     for (int q = 0; q < (WT == DT_F32 ? 4 : 2); ++q)
-        asm("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+        asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
             : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
             : "l"(p + 16 * q));
 }
 
-// h = RN(x + r), into x.
+// h = RN(x + r), into x.  16-bit types add in their own type: the sum of two
+// such values either is exact in binary32 or has one operand below a quarter
+// step of the other, so rounding once or through binary32 is the same.
 template <int DT>
 __device__ __forceinline__ void add_residual(Raw<DT> &x, const Raw<DT> &r)
 {
-    f2_t u[8], v[8];
-    to_pairs<DT>(x, u);
-    to_pairs<DT>(r, v);
+    if constexpr (DT == DT_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = f2_add(u[j], v[j]);
-    to_raw<DT>(u, x);
+        for (int j = 0; j < 16; ++j)
+            x.w[j] = __float_as_uint(__fadd_rn(__uint_as_float(x.w[j]), __uint_as_float(r.w[j])));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (DT == DT_BF16)
+                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(x.w[j]) : "r"(r.w[j]));
+            else
+                asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x.w[j]) : "r"(r.w[j]));
+        }
+    }
+}
+
+// A group's sum of squares added to s, s + s1 in two chains.  bf16 goes from its
+// packed words to the rebiased binary64 words directly (see add_square).
+template <int DT>
+__device__ __forceinline__ double add_group_squares(double s, const Raw<DT> &h)
+{
+    double s1 = 0.0;
+    if constexpr (DT == DT_BF16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w = h.w[j];
+            const uint32_t lo = (w & 0x7FFFu) * 8192u + 0x38000000u;
+            uint32_t hi;
+            asm("mad.hi.u32 %0, %1, %2, %3;"
+                : "=r"(hi) : "r"(w & 0x7FFF0000u), "r"(0x20000000u), "r"(0x38000000u));
+            const double x = __hiloint2double((int)lo, 0), y = __hiloint2double((int)hi, 0);
+            s = fma(x, x, s);
+            s1 = fma(y, y, s1);
+        }
+    } else {
+        f2_t v[8];
+        to_pairs<DT>(h, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float lo, hi;
+            f2_unpack(v[j], lo, hi);
+            s = add_square<DT>(s, lo);
+            s1 = add_square<DT>(s1, hi);
+        }
+    }
+    return s + s1;
+}
+
+// Rings in shared memory, one per warp: a warp copies the pieces that its
+// lanes will need of later rows there with cp.async and reads back only those,
+// so its lanes' wait_group and a __syncwarp order everything.  Loads in flight
+// then hold no registers, which the encoder needs.
+//
+// A warp's lanes own PP consecutive 16-byte pieces each.  They are copied with
+// neighbouring lanes on neighbouring pieces (each lane copying its own fetched every
+// 32-byte sector twice: 124 against 86 us for the norm of 8192 x 8192), and
+// placed so that eight lanes reading their q-th pieces hit different banks.
+template <int PP>
+__device__ __forceinline__ uint32_t piece_pos(uint32_t p)
+{
+    static_assert(PP == 1 || PP == 2 || PP == 4, "pieces per lane");
+    return 16u * (PP == 1 ? p : p ^ ((p >> 3) & (PP - 1)));
+}
+
+// Pieces p < valid of a warp's span, from src to ring (both the warp's).
+template <int PP>
+__device__ __forceinline__ void ring_copy(uint32_t ring, const char *src, int valid)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < PP; ++q) {
+        const int p = q * 32 + lane;
+        if (p < valid)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         :: "r"(ring + piece_pos<PP>(p)), "l"(src + p * 16) : "memory");
+    }
+}
+
+// This lane's PP pieces.
+template <int PP>
+__device__ __forceinline__ void ring_read(uint32_t ring, uint32_t *w)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < PP; ++q)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[4 * q]), "=r"(w[4 * q + 1]), "=r"(w[4 * q + 2]), "=r"(w[4 * q + 3])
+                     : "r"(ring + piece_pos<PP>(lane * PP + q)) : "memory");
+}
+
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// until at most N of the warp's newest groups are under way
+template <int N>
+__device__ __forceinline__ void ring_wait()
+{
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+    __syncwarp();
 }
 
 // h of one group: x, or RN(x + residual).
@@ -208,87 +321,92 @@ __device__ __forceinline__ void load_h(const NormArgs &a, int64_t row, int g, Ra
 
 // Rows of up to G groups per thread of the block: one pass, h kept in
 // registers between the sum and the encode (the weight comes from L1 each
-// time).  A block takes rows blockIdx.x, + gridDim.x, ...; with one or two
-// groups per thread, the next row's loads are issued as soon as h of a row is
-// formed (more groups leave no registers for it).
+// time).  A block takes rows blockIdx.x, + gridDim.x, ..., with the next S of
+// them under way in its threads' rings: 64 registers, 1024 threads per SM
+// whatever the block's size.
+//
+// Measured on IF4 8192 x 8192 bf16 with a residual, loads prefetched to
+// registers instead: one group per thread 92 us, two (128 registers, 512
+// threads per SM) 86-89 us.
 template <int DT, int G>
-constexpr int norm_blocks_per_sm()
-{
-    return G == 1 ? (DT == DT_F32 ? 3 : 4) : G == 2 ? 2 : 1;
-}
+struct NormRing {
+    static constexpr int S = DT != DT_F32 && G == 1 ? 2 : 1;     // rows under way
+    static constexpr int BYTES = S * 2 * G * 16 * elem_bytes<DT>();   // per thread: x, residual
+};
 
 template <int DT, int WT, int MODE, int G>
-__global__ void __launch_bounds__(G == 4 ? 512 : 256, norm_blocks_per_sm<DT, G>())
+__global__ void __launch_bounds__(1024, 1)
 rms_norm_quantize_rows_kernel(const __grid_constant__ NormArgs a)
 {
     pdl_enter();
+    using R = NormRing<DT, G>;
     __shared__ float inv_tab[128];
-    __shared__ double sums[2][16];
+    __shared__ double sums[2][32];
+    extern __shared__ __align__(16) uint8_t norm_ring[];
     constexpr int GB = 16 * elem_bytes<DT>();
-    const float ts = *a.ts;
+    constexpr int GP = elem_bytes<DT>();                     // pieces of a group
+    const float ts = ld_after_wait(a.ts);
     const float rts = __frcp_rn(ts);
     if (blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && a.err)
         atomicOr(a.err, IF4_DEV_BAD_SCALE);
     for (int i = threadIdx.x; i < 128; i += blockDim.x)
         inv_tab[i] = i == 0 ? 0.0f : __frcp_rn(__fmul_rn(f32_from_e4m3(i), ts));
-    constexpr bool PREFETCH = G == 1 || (G == 2 && DT != DT_F32);
-    Raw<DT> x[PREFETCH ? G : 1], r[PREFETCH ? G : 1];
-    auto fetch = [&](int64_t row) {
+    // a warp's ring: [stage][x, residual][group of the lane][span of 32 groups]
+    constexpr uint32_t SPAN = 32 * GB;
+    const int g0 = threadIdx.x & ~31;              // the warp's first group
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(norm_ring) +
+                          (threadIdx.x >> 5) * (32 * R::BYTES);
+    auto fetch = [&](int64_t row, int stage) {
+        __syncwarp();                      // the lanes have read what this overwrites
+        if (row < a.rows) {
 #pragma unroll
-        for (int k = 0; k < (PREFETCH ? G : 0); ++k) {
-            const int g = threadIdx.x + k * blockDim.x;
-            if (g < a.gpr) {
-                load_group_rw<DT>(a.x + row * a.ld_x + (int64_t)g * GB, x[k], a.v8);
-                if (a.res) load_group_rw<DT>(a.res + row * a.ld_res + (int64_t)g * GB, r[k], a.v8);
+            for (int k = 0; k < G; ++k) {
+                const int g = g0 + k * blockDim.x;
+                const uint32_t d = ring + (stage * 2 * G + k) * SPAN;
+                ring_copy<GP>(d, a.x + row * a.ld_x + (int64_t)g * GB, (a.gpr - g) * GP);
+                if (a.res)
+                    ring_copy<GP>(d + G * SPAN, a.res + row * a.ld_res + (int64_t)g * GB,
+                                  (a.gpr - g) * GP);
             }
         }
+        ring_commit();                     // also when empty: the waits count groups
     };
-#pragma unroll
-    for (int k = 0; k < (PREFETCH ? G : 0); ++k) {
-        zero_group(x[k]);
-        zero_group(r[k]);
-    }
     bool nonfinite = false;
     uint32_t top = 0;
-    int par = 0;
+    int par = 0, stage = 0;
     const int warps = blockDim.x >> 5;
     int64_t row = blockIdx.x;
-    if (PREFETCH && row < a.rows) fetch(row);
+#pragma unroll
+    for (int i = 0; i < R::S; ++i) fetch(row + (int64_t)i * gridDim.x, i);
     __syncthreads();                        // inv_tab
     for (; row < a.rows; row += gridDim.x, par ^= 1) {
+        ring_wait<R::S - 1>();
         double s = 0.0;
         Raw<DT> h[G];
 #pragma unroll
         for (int k = 0; k < G; ++k) {
-            if constexpr (PREFETCH) {
-                h[k] = x[k];
-                if (a.res) add_residual<DT>(h[k], r[k]);
-            } else {
-                const int g = threadIdx.x + k * blockDim.x;
-                zero_group(h[k]);
-                if (g < a.gpr) load_h<DT>(a, row, g, h[k]);
+            zero_group(h[k]);
+            if (threadIdx.x + k * blockDim.x < a.gpr) {
+                const uint32_t d = ring + (stage * 2 * G + k) * SPAN;
+                ring_read<GP>(d, h[k].w);
+                if (a.res) {
+                    Raw<DT> r;
+                    ring_read<GP>(d + G * SPAN, r.w);
+                    add_residual<DT>(h[k], r);
+                }
             }
-            f2_t v[8];
-            to_pairs<DT>(h[k], v);
-            double s0 = 0.0, s1 = 0.0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float lo, hi;
-                f2_unpack(v[j], lo, hi);
-                s0 = fma((double)lo, (double)lo, s0);
-                s1 = fma((double)hi, (double)hi, s1);
-            }
-            s += s0 + s1;
+            s = add_group_squares<DT>(s, h[k]);
         }
-        // h may be x's or the residual's memory: this row's store only comes
-        // after this row's loads, and no other block reads this row
+        fetch(row + (int64_t)R::S * gridDim.x, stage);
+        if (++stage == R::S) stage = 0;
+        // h may be x's or the residual's memory: a warp stores only what it
+        // has copied itself, and no other warp reads that
 #pragma unroll
         for (int k = 0; k < G; ++k) {
             const int g = threadIdx.x + k * blockDim.x;
             if (a.h && g < a.gpr)
                 store_group<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h[k], a.v8);
         }
-        if (PREFETCH && row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (warps > 1) {
@@ -296,8 +414,10 @@ rms_norm_quantize_rows_kernel(const __grid_constant__ NormArgs a)
             // barrier of row i + 1, which every reader of row i's has passed
             if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = s;
             __syncthreads();
-            s = sums[par][0];
-            for (int i = 1; i < warps; ++i) s += sums[par][i];
+            const int i = threadIdx.x & 31;
+            s = i < warps ? sums[par][i] : 0.0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         }
         const float rstd = row_rstd(s, a.inv_cols, a.eps);
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
@@ -346,7 +466,7 @@ rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
     pdl_enter();
     __shared__ float inv_tab[128];
     __shared__ double sums[NORM_THREADS / 32];
-    const float ts = *a.ts;
+    const float ts = ld_after_wait(a.ts);
     const float rts = __frcp_rn(ts);
     if (blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && a.err)
         atomicOr(a.err, IF4_DEV_BAD_SCALE);
@@ -365,8 +485,8 @@ rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
             for (int j = 0; j < 8; ++j) {
                 float lo, hi;
                 f2_unpack(v[j], lo, hi);
-                s = fma((double)lo, (double)lo, s);
-                s = fma((double)hi, (double)hi, s);
+                s = add_square<DT>(s, lo);
+                s = add_square<DT>(s, hi);
             }
         }
         s = block_sum(s, sums);
@@ -379,7 +499,7 @@ rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
             f2_t v[8], w[8];
             load_h<DT>(a, row, g, h);
             if (a.h) store_group<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h);
-            load_group<WT, false>(a.w + (int64_t)g * 16 * elem_bytes<WT>(), wr);
+            load_weight<WT>(a.w, g, wr);
             to_pairs<DT>(h, v);
             to_pairs<WT>(wr, w);
             uint32_t m = 0;
@@ -423,62 +543,130 @@ struct BackArgs {
     float inv_cols;
 };
 
-// Rows of up to 1024 groups (G per thread): one pass over dy, h and dres.  A
-// block of 512 threads holds 512 / T rows at a time, T threads each (a power
-// of two, at least a warp); a thread keeps its columns' part of dw in
-// registers over all its rows.  The row sums meet at a barrier of the row's
-// own threads.  At the end the block's row slots add their parts through
-// shared memory, and the block writes one partial row.
-template <int DT, int WT, int G>
-__global__ void __launch_bounds__(512, G == 1 && DT != DT_F32 ? 2 : 1)
+// The gradient's rows kernel works in units of 8 elements, so that dw of a
+// unit (8 floats), the weight and a row's inputs fit 64 registers.
+template <int DT>
+struct Unit {
+    static constexpr int BYTES = 8 * elem_bytes<DT>();
+    uint32_t w[DT == DT_F32 ? 8 : 4];
+};
+
+// Pair j (elements 2j, 2j + 1) in binary32.
+template <int DT>
+__device__ __forceinline__ f2_t pair_of(const Unit<DT> &r, int j)
+{
+    if constexpr (DT == DT_F32)
+        return f2_pack(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+    else if constexpr (DT == DT_BF16)
+        return f2_from_bf16x2(r.w[j]);
+    else
+        return f2_pack(f16lo_to_f32(r.w[j]), f16hi_to_f32(r.w[j]));
+}
+
+template <int DT, int U>
+struct BackRing {
+    static constexpr int S = DT != DT_F32 && U == 1 ? 4 : 2;     // rows under way
+    static constexpr int BYTES = S * 3 * U * Unit<DT>::BYTES;    // per thread: h, dy, dres
+};
+
+// Rows of up to U * T units: one pass over dy, h and dres.  A block of
+// `slots` x T threads holds `slots` rows at a time, T threads each (a power of
+// two, at least a warp), with the next S rows of each slot under way in its
+// threads' rings; a thread keeps its columns' part of dw in registers over all
+// its rows.  The row sums meet at a barrier of the row's own threads.  At the
+// end the block's row slots add their parts through shared memory, and the
+// block writes one partial row.  Loads prefetched to registers, one row ahead,
+// spilled and left memory waits: 16384 x 4096 bf16 115 us.
+template <int DT, int WT, int U>
+__global__ void __launch_bounds__(U == 1 ? 1024 : 512, 1)
 rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
 {
     pdl_enter();
-    constexpr int GB = 16 * elem_bytes<DT>();
-    __shared__ float sums[2][16];
-    extern __shared__ float slot_dw[];              // [slots - 1][cols]
-    const int slots = 512 / T, slot = threadIdx.x / T, t = threadIdx.x % T;
+    using R = BackRing<DT, U>;
+    constexpr int UP = elem_bytes<DT>() / 2;        // pieces of a unit
+    __shared__ float sums[2][32];
+    extern __shared__ __align__(16) uint8_t back_smem[];   // the rings, then [slots - 1][cols]
+    const int slots = blockDim.x / T, slot = threadIdx.x / T, t = threadIdx.x % T;
     const int warps = T >> 5, warp0 = slot * warps;
-    f2_t dw[G][8];
+    const int units = a.gpr * 2;
+    const int64_t step = (int64_t)gridDim.x * slots;
+    // the weight: in registers with one unit per thread, from L1 with more
+    auto weight = [&](int u) {
+        Unit<WT> r;
 #pragma unroll
-    for (int k = 0; k < G; ++k)
+        for (uint32_t &z : r.w) z = 0u;
+        if (u < units) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] = f2_pack(0.0f, 0.0f);
-    int par = 0;
-    for (int64_t row = (int64_t)blockIdx.x * slots + slot; row < a.rows;
-         row += (int64_t)gridDim.x * slots, par ^= 1) {
-        const float rstd = a.rstd[row];
-        Raw<DT> h[G], d[G], e[G];
-#pragma unroll
-        for (int k = 0; k < G; ++k) {
-            const int g = t + k * T;
-            zero_group(h[k]);
-            zero_group(d[k]);
-            zero_group(e[k]);
-            if (g < a.gpr) {
-                load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h[k], a.v8);
-                load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, d[k], a.v8);
-                if (a.dres)
-                    load_group_rw<DT>(a.dres + row * a.ld_dres + (int64_t)g * GB, e[k], a.v8);
-            }
+            for (int q = 0; q < (WT == DT_F32 ? 2 : 1); ++q)
+                asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                    : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]),
+                      "=r"(r.w[4 * q + 3])
+                    : "l"(a.w + (int64_t)u * Unit<WT>::BYTES + 16 * q));
         }
+        return r;
+    };
+    const Unit<WT> w1 = weight(t);
+    f2_t dw[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[k][j] = f2_pack(0.0f, 0.0f);
+    // a warp's ring: [stage][h, dy, dres][unit of the lane][span of 32 units]
+    constexpr uint32_t SPAN = 32 * Unit<DT>::BYTES;
+    const int u0 = t & ~31;                         // the warp's first unit
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(back_smem) +
+                          (threadIdx.x >> 5) * (32 * R::BYTES);
+    auto fetch = [&](int64_t row, int stage) {
+        __syncwarp();                      // the lanes have read what this overwrites
+        if (row < a.rows) {
+            auto copy = [&](const char *src, int64_t ld, int which) {
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int u = u0 + k * T;
+                    ring_copy<UP>(ring + ((stage * 3 + which) * U + k) * SPAN,
+                                  src + row * ld + (int64_t)u * Unit<DT>::BYTES, (units - u) * UP);
+                }
+            };
+            copy(a.h, a.ld_h, 0);
+            copy(a.dy, a.ld_dy, 1);
+            if (a.dres) copy(a.dres, a.ld_dres, 2);
+        }
+        ring_commit();                     // also when empty: the waits count groups
+    };
+    int par = 0, stage = 0;
+    int64_t row = (int64_t)blockIdx.x * slots + slot;
+    // dx may be dy's or dres's memory: a warp stores only what it has copied
+    // itself, and no other warp reads that
+#pragma unroll
+    for (int i = 0; i < R::S; ++i) fetch(row + i * step, i);
+    float rstd_next = row < a.rows ? a.rstd[row] : 0.0f;
+    for (; row < a.rows; row += step, par ^= 1) {
+        ring_wait<R::S - 1>();
+        const float rstd = rstd_next;
+        if (row + step < a.rows) rstd_next = a.rstd[row + step];
+        // one unit stays in registers over the sum; more are read a second time
+        Unit<DT> h, d, e;
+        auto read = [&](int k, bool with_e) {
+            const uint32_t r = ring + (stage * 3 * U + k) * SPAN;
+            ring_read<UP>(r, h.w);
+            ring_read<UP>(r + U * SPAN, d.w);
+            if (with_e && a.dres) ring_read<UP>(r + 2 * U * SPAN, e.w);
+        };
         f2_t acc = f2_pack(0.0f, 0.0f);
         const f2_t RS = f2_pack(rstd, rstd);
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-            f2_t hv[8], dv[8], wv[8];
-            Raw<WT> w;
-            load_weight<WT>(a.w, min(t + k * T, a.gpr - 1), w);
-            to_pairs<DT>(h[k], hv);
-            to_pairs<DT>(d[k], dv);
-            to_pairs<WT>(w, wv);
+        for (int k = 0; k < U; ++k)
+            if (t + k * T < units) {
+                read(k, U == 1);
+                const Unit<WT> w = U == 1 ? w1 : weight(t + k * T);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const f2_t dh = f2_mul(dv[j], hv[j]);
-                acc = f2_fma(dh, wv[j], acc);
-                dw[k][j] = f2_fma(dh, RS, dw[k][j]);
+                for (int j = 0; j < 4; ++j) {
+                    const f2_t dh = f2_mul(pair_of(d, j), pair_of(h, j));
+                    acc = f2_fma(dh, pair_of(w, j), acc);
+                    dw[k][j] = f2_fma(dh, RS, dw[k][j]);
+                }
             }
-        }
+        if constexpr (U == 1) fetch(row + R::S * step, stage);
         float s, hi;
         f2_unpack(acc, s, hi);
         s += hi;
@@ -487,62 +675,74 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
         if (warps > 1) {
             // two buffers in turn: see the forward kernel
             if ((threadIdx.x & 31) == 0) sums[par][threadIdx.x >> 5] = s;
+            // (barrier 0 is __syncthreads', below)
             asm volatile("bar.sync %0, %1;" :: "r"(slot + 1), "r"(T) : "memory");
-            s = sums[par][warp0];
-            for (int i = 1; i < warps; ++i) s += sums[par][warp0 + i];
+            const int i = threadIdx.x & 31;
+            s = i < warps ? sums[par][warp0 + i] : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         }
         // mean(g * n) * rstd, n = h * rstd
         const float c = s * rstd * rstd * a.inv_cols;
         const f2_t NC = f2_pack(-c, -c);
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-            const int g = t + k * T;
-            if (g < a.gpr) {
-                f2_t hv[8], dv[8], wv[8], ev[8];
-                Raw<WT> w;
-                load_weight<WT>(a.w, g, w);
-                to_pairs<DT>(h[k], hv);
-                to_pairs<DT>(d[k], dv);
-                to_pairs<WT>(w, wv);
-                to_pairs<DT>(e[k], ev);
+        for (int k = 0; k < U; ++k) {
+            const int u = t + k * T;
+            if (u < units) {
+                if constexpr (U > 1) read(k, true);
+                const Unit<WT> w = U == 1 ? w1 : weight(u);
+                uint32_t o[DT == DT_F32 ? 8 : 4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const f2_t v = f2_mul(f2_fma(hv[j], NC, f2_mul(dv[j], wv[j])), RS);
-                    dv[j] = a.dres ? f2_add(v, ev[j]) : v;
+                for (int j = 0; j < 4; ++j) {
+                    f2_t v = f2_mul(f2_fma(pair_of(h, j), NC,
+                                           f2_mul(pair_of(d, j), pair_of(w, j))), RS);
+                    if (a.dres) v = f2_add(v, pair_of(e, j));
+                    float lo, up;
+                    f2_unpack(v, lo, up);
+                    if constexpr (DT == DT_F32) {
+                        o[2 * j] = __float_as_uint(lo);
+                        o[2 * j + 1] = __float_as_uint(up);
+                    } else {
+                        o[j] = DT == DT_BF16 ? bf16x2_from_f32(lo, up) : f16x2_from_f32(lo, up);
+                    }
                 }
-                Raw<DT> o;
-                to_raw<DT>(dv, o);
-                store_group<DT>(a.dx + row * a.ld_dx + (int64_t)g * GB, o, a.v8);
+                char *p = a.dx + row * a.ld_dx + (int64_t)u * Unit<DT>::BYTES;
+#pragma unroll
+                for (int q = 0; q < (DT == DT_F32 ? 2 : 1); ++q)
+                    st_v4(p + 16 * q, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
         }
+        if constexpr (U > 1) fetch(row + R::S * step, stage);
+        if (++stage == R::S) stage = 0;
     }
     // the block's partial row: slot 0 adds the others' in order
     const int cols = a.gpr * 16;
+    float *slot_dw = reinterpret_cast<float *>(back_smem + blockDim.x * R::BYTES);
     if (slots > 1) {
         if (slot > 0)
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const int g = t + k * T;
-                if (g < a.gpr)
+            for (int k = 0; k < U; ++k) {
+                const int u = t + k * T;
+                if (u < units)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<f2_t *>(slot_dw + (slot - 1) * cols + g * 16 + 2 * j) = dw[k][j];
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<f2_t *>(slot_dw + (slot - 1) * cols + u * 8 + 2 * j) = dw[k][j];
             }
         __syncthreads();
     }
     if (slot == 0)
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-            const int g = t + k * T;
-            if (g < a.gpr) {
+        for (int k = 0; k < U; ++k) {
+            const int u = t + k * T;
+            if (u < units) {
                 for (int q = 0; q < slots - 1; ++q)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < 4; ++j)
                         dw[k][j] = f2_add(dw[k][j], *reinterpret_cast<const f2_t *>(
-                                                        slot_dw + q * cols + g * 16 + 2 * j));
-                float *p = a.part + (int64_t)blockIdx.x * cols + g * 16;
+                                                        slot_dw + q * cols + u * 8 + 2 * j));
+                float *p = a.part + (int64_t)blockIdx.x * cols + u * 8;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) *reinterpret_cast<f2_t *>(p + 2 * j) = dw[k][j];
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<f2_t *>(p + 2 * j) = dw[k][j];
             }
         }
 }
@@ -565,7 +765,7 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
             f2_t h[8], d[8], w[8];
             load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr);
             load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr);
-            load_group<WT, false>(a.w + (int64_t)g * 16 * elem_bytes<WT>(), wr);
+            load_weight<WT>(a.w, g, wr);
             to_pairs<DT>(hr, h);
             to_pairs<DT>(dr, d);
             to_pairs<WT>(wr, w);
@@ -586,7 +786,7 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
             f2_t h[8], d[8], w[8], e[8];
             load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr);
             load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr);
-            load_group<WT, false>(a.w + (int64_t)g * 16 * elem_bytes<WT>(), wr);
+            load_weight<WT>(a.w, g, wr);
             to_pairs<DT>(hr, h);
             to_pairs<DT>(dr, d);
             to_pairs<WT>(wr, w);
@@ -633,7 +833,7 @@ rms_norm_dw_kernel(const __grid_constant__ BackArgs a)
 // dw: n partial rows.  A block takes 32 columns; warp v adds rows v, v + 32,
 // ..., then one warp adds the 32 sums in order.
 __global__ void __launch_bounds__(1024)
-rms_norm_dw_sum_kernel(const float *__restrict__ part, int n, int cols, float *__restrict__ dw)
+rms_norm_dw_sum_kernel(const float *part, int n, int cols, float *dw)
 {
     pdl_enter();
     __shared__ float sums[32][33];
@@ -641,7 +841,7 @@ rms_norm_dw_sum_kernel(const float *__restrict__ part, int n, int cols, float *_
     const int col = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (col < cols)
-        for (int i = v; i < n; i += 32) s += part[(int64_t)i * cols + col];
+        for (int i = v; i < n; i += 32) s += ld_after_wait(part + (int64_t)i * cols + col);
     sums[v][lane] = s;
     __syncthreads();
     if (v == 0 && col < cols) {
@@ -672,6 +872,38 @@ int by_types(int x_dtype, int w_dtype, F f)
     if (x_dtype == IF4_F32) return f(F32{}, F32{});
     if (x_dtype == IF4_BF16) return w_dtype == IF4_F32 ? f(BF{}, F32{}) : f(BF{}, BF{});
     return w_dtype == IF4_F32 ? f(HF{}, F32{}) : f(HF{}, HF{});
+}
+
+// Programmatic launch with dynamic shared memory (at most `most` bytes, allowed
+// once per kernel and device).
+template <typename... KArgs, typename... Args>
+int launch_rows(void (*kernel)(KArgs...), unsigned grid, unsigned threads, unsigned smem,
+                unsigned most, const DeviceInfo &d, cudaStream_t st, Args... args)
+{
+    if (smem > 48 * 1024) {
+        static std::mutex mu;
+        static std::set<std::pair<const void *, int>> allowed;
+        std::lock_guard<std::mutex> lock(mu);
+        const auto key = std::make_pair(reinterpret_cast<const void *>(kernel), d.id);
+        if (!allowed.count(key)) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)most) != cudaSuccess)
+                return IF4_ERR_CUDA;
+            allowed.insert(key);
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return IF4_ERR_CUDA;
+    return launch_status();
 }
 
 template <int MODE>
@@ -706,17 +938,19 @@ int rms_norm_quantize_entry(const void *x, int64_t ld_x, const void *res, int64_
     return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
         constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
         const int64_t warps = (n + 31) / 32;
-        auto rows_kernel = [&](auto k, auto G) {
-            constexpr int g = decltype(G)::value, per_sm = norm_blocks_per_sm<DT, g>();
+        auto rows_kernel = [&](auto G) {
+            constexpr int g = decltype(G)::value;
             // the fewest whole warps that hold a row; blocks for one wave
             const unsigned threads = (unsigned)((warps + g - 1) / g * 32);
-            const int64_t wave = (int64_t)d.sm_count * per_sm * (256 / threads ? 256 / threads : 1);
-            return launch_k(k, (unsigned)std::min(rows, wave), threads, st, a);
+            const unsigned per_sm = std::min<unsigned>(1024 / threads, 32);
+            return launch_rows(rms_norm_quantize_rows_kernel<DT, WT, MODE, g>,
+                               (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * per_sm),
+                               threads, threads * NormRing<DT, g>::BYTES,
+                               1024 * NormRing<DT, g>::BYTES, d, st, a);
         };
-        if (n <= 256) return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 1>, std::integral_constant<int, 1>{});
-        if (n <= 512) return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 2>, std::integral_constant<int, 2>{});
-        if (n <= (DT == DT_F32 ? 1024 : 2048))
-            return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 4>, std::integral_constant<int, 4>{});
+        if (n <= 1024) return rows_kernel(std::integral_constant<int, 1>{});
+        if constexpr (DT != DT_F32)
+            if (n <= 2048) return rows_kernel(std::integral_constant<int, 2>{});
         return launch_k(rms_norm_quantize_kernel<DT, WT, MODE>,
                         (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8),
                         (unsigned)NORM_THREADS, st, a);
@@ -794,25 +1028,30 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
     };
     return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
         constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
-        if (n <= 1024) {
+        if (n <= (DT == DT_F32 ? 512 : 1024)) {
+            // up to 8192 columns one unit per thread, blocks of 512 threads (two
+            // per SM) or, above 4096 columns, 1024; then 512 threads, four units
+            const int64_t units = 2 * n;
             int T = 32;
-            while (T < 512 && T < n) T *= 2;
-            const int slots = 512 / T;
-            const int parts = (int)std::min<int64_t>((rows + slots - 1) / slots, BACK_BLOCKS);
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)parts, 1, 1);
-            cfg.blockDim = dim3(512, 1, 1);
-            cfg.dynamicSmemBytes = (size_t)(slots - 1) * (size_t)cols * sizeof(float);
-            cfg.stream = st;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[0].val.programmaticStreamSerializationAllowed = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            const cudaError_t e =
-                n <= 512 ? cudaLaunchKernelEx(&cfg, rms_norm_backward_rows_kernel<DT, WT, 1>, a, T)
-                         : cudaLaunchKernelEx(&cfg, rms_norm_backward_rows_kernel<DT, WT, 2>, a, T);
-            if (e != cudaSuccess) return (int)IF4_ERR_CUDA;
+            while (T < 1024 && T < units) T *= 2;
+            if (units > 1024) T = 512;
+            const int threads = std::max(T, 512), slots = threads / T;
+            const int parts = (int)std::min<int64_t>((rows + slots - 1) / slots,
+                                                     units > 512 ? BACK_BLOCKS / 2 : BACK_BLOCKS);
+            auto rows_kernel = [&](auto V) {
+                constexpr int U = decltype(V)::value;
+                const unsigned smem = threads * BackRing<DT, U>::BYTES +
+                                      (unsigned)((slots - 1) * cols * sizeof(float));
+                return launch_rows(rms_norm_backward_rows_kernel<DT, WT, U>, (unsigned)parts,
+                                   (unsigned)threads, smem, 227u * 1024u - 512u, d, st, a, T);
+            };
+            int r;
+            if constexpr (DT != DT_F32)
+                r = units <= 1024 ? rows_kernel(std::integral_constant<int, 1>{})
+                                  : rows_kernel(std::integral_constant<int, 4>{});
+            else
+                r = rows_kernel(std::integral_constant<int, 1>{});
+            if (r != IF4_OK) return r;
             return sum_dw(parts);
         }
         const int parts = (int)std::min<int64_t>(rows, BACK_BLOCKS);

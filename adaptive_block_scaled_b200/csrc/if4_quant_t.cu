@@ -9,13 +9,19 @@
 //   dW = dY^T X   contracts over M: dY^T and X^T grouped along M,
 // so each of X, W and dY is needed both ways.
 //
-// A block takes a tile of 128 x 128.  Each thread loads whole row groups (16
-// values, 32 or 64 bytes), encodes them when the row form is wanted, and
-// leaves the raw values in shared memory.  Then a thread reads 16 rows of two
-// neighbouring columns (one conflict-free word per row), which are two whole
-// column groups in registers, and encodes them with the same group encoder.
-// The column codes are put back in order through shared memory, so that the
-// tile's 64 code bytes of a column leave as one run.
+// A block takes a tile of 128 x 128 into shared memory with asynchronous
+// 16-byte copies, which hold no registers while they are under way.  Row form:
+// a thread reads whole row groups (16 values, 32 or 64 bytes) and encodes them.
+// Column form: a thread reads 16 rows of two neighbouring columns (one
+// conflict-free word per row), which are two whole column groups in registers,
+// and encodes them with the same group encoder.  The column codes are put back
+// in order through shared memory, so that the tile's 64 code bytes of a column
+// leave as one run.
+//
+// With both forms and IF4 the encoder's instructions bound it (two encodes of
+// about 200 instructions per 16 values; 8192 x 8192 bf16, tensor scale given);
+// four blocks per SM keep 32 warps issuing.  Holding the tile's loads in
+// registers instead allowed two: 83 us.
 
 #include <cuda_runtime.h>
 
@@ -47,13 +53,24 @@ __host__ __device__ constexpr int smem_t_bytes()
     return tile_bytes<DT>() + TILE * CODE_PITCH + TILE * TG;
 }
 
-__device__ __forceinline__ void sts_v4(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+// Byte offset of 16-byte piece k of a tile row.  The pieces are permuted inside
+// each 128 bytes so that the eight lanes that read the same piece of eight
+// neighbouring row groups hit different banks; a whole row read by columns is
+// a permutation of the same banks.
+template <int DT>
+__device__ __forceinline__ int piece_at(int k)
 {
-    *static_cast<uint4 *>(p) = make_uint4(a, b, c, d);
+    return 16 * (DT == DT_F32 ? k ^ ((k >> 3) & 3) : k ^ ((k >> 3) & 1));
 }
 
-template <int DT, int MODE, bool ROWS, bool V8>
-__global__ void __launch_bounds__(THREADS_T)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+template <int DT, int MODE, bool ROWS>
+__global__ void __launch_bounds__(THREADS_T, DT == DT_F32 ? 2 : 4)
 quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, int64_t cols,
                   uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                   uint8_t *__restrict__ codes_t, uint8_t *__restrict__ scales_t,
@@ -61,118 +78,116 @@ quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, in
 {
     pdl_enter();
     constexpr int ES = elem_bytes<DT>();
-    constexpr int GB = 16 * ES;
     constexpr int PITCH = TILE * ES;
+    constexpr int PIECES = PITCH / 16;      // 16-byte pieces of a tile row
+    constexpr int GP = ES;                  // pieces of a group: 2 or 4
     extern __shared__ __align__(16) uint8_t smem_t[];
     uint8_t *tile = smem_t;
     uint8_t *code_out = smem_t + tile_bytes<DT>();
     uint8_t *scale_out = code_out + TILE * CODE_PITCH;
     __shared__ float inv_tab[128];
 
-    const float ts = *ts_ptr;
+    const int64_t col_tiles = (cols + TILE - 1) / TILE;
+    const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)col_tiles) * TILE;
+    const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_tiles) * TILE;
+    const int tile_rows = (int)min((int64_t)TILE, rows - r0);
+    const int tile_cols = (int)min((int64_t)TILE, cols - c0);
+    {
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(tile);
+        const char *src = x + r0 * ld_bytes + c0 * ES;
+        const int k = threadIdx.x % PIECES;
+#pragma unroll
+        for (int i = 0; i < TILE * PIECES / THREADS_T; ++i) {
+            const int r = threadIdx.x / PIECES + i * (THREADS_T / PIECES);
+            // past the tensor: zero fill, the address stays inside it
+            const bool in = r < tile_rows && k * 16 < tile_cols * ES;
+            cp_async16(dst + r * PITCH + piece_at<DT>(k),
+                       in ? src + (int64_t)r * ld_bytes + k * 16 : x, in);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    const float ts = ld_after_wait(ts_ptr);
     const float rts = __frcp_rn(ts);
     if (check_ts && blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && err)
         atomicOr(err, IF4_DEV_BAD_SCALE);
     fill_inv_tab(inv_tab, ts);
-
-    const int64_t col_tiles = (cols + TILE - 1) / TILE;
-    const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)col_tiles) * TILE;
-    const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_tiles) * TILE;
-    bool nonfinite = false;
-
-    // row groups: thread t takes group t % 8 of rows t / 8, + 32, + 64, + 96
-    const int lg = threadIdx.x & (TG - 1), lr = threadIdx.x / TG;
-    Raw<DT> raw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + lr + 32 * i, c = c0 + 16 * lg;
-        if (r < rows && c < cols) {
-            load_group<DT, V8>(x + r * ld_bytes + c * ES, raw[i]);
-        } else {
-#pragma unroll
-            for (uint32_t &w : raw[i].w) w = 0u;
-        }
-    }
-    __syncthreads();                        // inv_tab
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = lr + 32 * i;
-        uint8_t *d = tile + row * PITCH + lg * GB;
-        // 16-byte pieces in an order that keeps the eight lanes of a store
-        // phase on different banks
-        constexpr int PIECES = GB / 16;
-#pragma unroll
-        for (int q = 0; q < PIECES; ++q) {
-            const int k = ES == 2 ? (q ^ ((lg >> 2) & 1)) : ((q + (lg >> 1)) & 3);
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = raw[i].w[e];
-#pragma unroll
-                for (int z = 1; z < PIECES; ++z) v[e] = k == z ? raw[i].w[4 * z + e] : v[e];
-            }
-            sts_v4(d + 16 * k, v[0], v[1], v[2], v[3]);
-        }
-        if constexpr (ROWS) {
-            const int64_t r = r0 + row, c = c0 + 16 * lg;
-            if (r < rows && c < cols) {
-                f2_t xv[8];
-                bool bad;
-                const float amax = unpack_group<DT>(raw[i], xv, bad);
-                const GroupCode g = encode_registers<MODE>(xv, amax, ts, rts, inv_tab);
-                const int64_t gi = r * (cols / 16) + c / 16;
-                st_v2(codes + gi * 8, g.c0, g.c1);
-                st_u8(scales + gi, g.scale);
-            }
-        }
-    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
+
+    if constexpr (ROWS) {
+        // thread t takes group t % 8 of rows t / 8, + 32, + 64, + 96
+        const int lg = threadIdx.x & (TG - 1);
+#pragma unroll 1
+        for (int row = threadIdx.x / TG; row < tile_rows; row += THREADS_T / TG) {
+            if (16 * lg >= tile_cols) break;
+            Raw<DT> raw;
+#pragma unroll
+            for (int q = 0; q < GP; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * PITCH +
+                                                                 piece_at<DT>(lg * GP + q));
+                raw.w[4 * q] = v.x;
+                raw.w[4 * q + 1] = v.y;
+                raw.w[4 * q + 2] = v.z;
+                raw.w[4 * q + 3] = v.w;
+            }
+            f2_t xv[8];
+            bool bad;                       // the column form reports it
+            const float amax = unpack_group<DT>(raw, xv, bad);
+            const GroupCode g = encode_registers<MODE>(xv, amax, ts, rts, inv_tab);
+            const int64_t gi = (r0 + row) * (cols / 16) + c0 / 16 + lg;
+            st_v2(codes + gi * 8, g.c0, g.c1);
+            st_u8(scales + gi, g.scale);
+        }
+    }
 
     // column groups: warp w takes row group w, a lane two neighbouring
     // columns of each half of the tile
+    bool nonfinite = false;
     const int rg = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (16 * rg < tile_rows) {
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        const int col = h * (TILE / 2) + 2 * lane;
-        const uint8_t *p = tile + rg * 16 * PITCH + col * ES;
-        Raw<DT> a, b;
-        if constexpr (DT == DT_F32) {
+        for (int col = 2 * lane; col < tile_cols; col += TILE / 2) {
+            const uint8_t *p = tile + rg * 16 * PITCH + piece_at<DT>(col * ES / 16) + col * ES % 16;
+            Raw<DT> a, b;
+            if constexpr (DT == DT_F32) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(p + i * PITCH);
-                a.w[i] = w.x;
-                b.w[i] = w.y;
+                for (int i = 0; i < 16; ++i) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(p + i * PITCH);
+                    a.w[i] = w.x;
+                    b.w[i] = w.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u = *reinterpret_cast<const uint32_t *>(p + 2 * i * PITCH);
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(p + (2 * i + 1) * PITCH);
+                    a.w[i] = if4dev::prmt(u, v, 0x5410u);
+                    b.w[i] = if4dev::prmt(u, v, 0x7632u);
+                }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t u = *reinterpret_cast<const uint32_t *>(p + 2 * i * PITCH);
-                const uint32_t v = *reinterpret_cast<const uint32_t *>(p + (2 * i + 1) * PITCH);
-                a.w[i] = if4dev::prmt(u, v, 0x5410u);
-                b.w[i] = if4dev::prmt(u, v, 0x7632u);
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                f2_t xv[8];
+                bool bad;
+                const float amax = unpack_group<DT>(a, xv, bad);
+                nonfinite |= bad;
+                const GroupCode g = encode_registers<MODE>(xv, amax, ts, rts, inv_tab);
+                *reinterpret_cast<uint2 *>(code_out + (col + k) * CODE_PITCH + rg * 8) =
+                    make_uint2(g.c0, g.c1);
+                scale_out[(col + k) * TG + rg] = (uint8_t)g.scale;
+                a = b;
             }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            f2_t xv[8];
-            bool bad;
-            const float amax = unpack_group<DT>(k ? b : a, xv, bad);
-            nonfinite |= bad;
-            const GroupCode g = encode_registers<MODE>(xv, amax, ts, rts, inv_tab);
-            *reinterpret_cast<uint2 *>(code_out + (col + k) * CODE_PITCH + rg * 8) =
-                make_uint2(g.c0, g.c1);
-            scale_out[(col + k) * TG + rg] = (uint8_t)g.scale;
         }
     }
     __syncthreads();
+    const int row_groups = tile_rows / 16;
 #pragma unroll
     for (int i = 0; i < TILE * TG / THREADS_T; ++i) {
         const int k = threadIdx.x + i * THREADS_T;
         const int col = k / TG, g = k & (TG - 1);
-        const int64_t c = c0 + col, rgrp = r0 / 16 + g;
-        if (c < cols && rgrp < rows / 16) {
+        if (col < tile_cols && g < row_groups) {
             const uint2 w = *reinterpret_cast<const uint2 *>(code_out + col * CODE_PITCH + g * 8);
-            const int64_t gi = c * (rows / 16) + rgrp;
+            const int64_t gi = (c0 + col) * (rows / 16) + r0 / 16 + g;
             st_v2(codes_t + gi * 8, w.x, w.y);
             st_u8(scales_t + gi, scale_out[col * TG + g]);
         }
@@ -186,11 +201,11 @@ struct OutT {
     uint8_t *codes, *scales, *codes_t, *scales_t;
 };
 
-template <int DT, int MODE, bool ROWS, bool V8>
+template <int DT, int MODE, bool ROWS>
 int launch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t cols, const OutT &o,
                       const float *ts, int *err, int check_ts, cudaStream_t st, const DeviceInfo &d)
 {
-    auto kernel = quantize_t_kernel<DT, MODE, ROWS, V8>;
+    auto kernel = quantize_t_kernel<DT, MODE, ROWS>;
     constexpr int SMEM = smem_t_bytes<DT>();
     static std::once_flag once[MAX_DEVICES];
     static cudaError_t rcs[MAX_DEVICES];
@@ -221,11 +236,8 @@ int dispatch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t col
                         const float *ts, int *err, int check_ts, cudaStream_t st,
                         const DeviceInfo &d)
 {
-    if (o.codes)
-        return s.v8 ? launch_quantize_t<DT, MODE, true, true>(s, x, rows, cols, o, ts, err, check_ts, st, d)
-                    : launch_quantize_t<DT, MODE, true, false>(s, x, rows, cols, o, ts, err, check_ts, st, d);
-    return s.v8 ? launch_quantize_t<DT, MODE, false, true>(s, x, rows, cols, o, ts, err, check_ts, st, d)
-                : launch_quantize_t<DT, MODE, false, false>(s, x, rows, cols, o, ts, err, check_ts, st, d);
+    return o.codes ? launch_quantize_t<DT, MODE, true>(s, x, rows, cols, o, ts, err, check_ts, st, d)
+                   : launch_quantize_t<DT, MODE, false>(s, x, rows, cols, o, ts, err, check_ts, st, d);
 }
 
 template <int MODE>

@@ -388,7 +388,7 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
         const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(acc_full), 0, abort_flag));
         tc_fence_after();
         if (ok && u0 < u1) {
-            const float scale = __fmul_rn(*x_ts, *w_ts);
+            const float scale = __fmul_rn(ld_after_wait(x_ts), ld_after_wait(w_ts));
             float *part = reinterpret_cast<float *>(smem);
 #pragma unroll 1
             for (int mc = 0; mc < NT && m0 + mc < M; mc += 16) {
@@ -414,7 +414,7 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
         // rank r adds tokens r, r + ranks, ...: a warp per token, four rows per
         // lane, the partials of all ranks loaded before they are added in order
         if (!*abort_flag) {
-            const float scale = __fmul_rn(*x_ts, *w_ts);
+            const float scale = __fmul_rn(ld_after_wait(x_ts), ld_after_wait(w_ts));
             uint32_t part[MAX_RANKS];
 #pragma unroll
             for (uint32_t s = 0; s < MAX_RANKS; ++s)
@@ -818,7 +818,7 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
     } else if (warp >= 2) {
         // -------------------------------------------------------- epilogue
         const int quarter = warp & 3;
-        const float scale = __fmul_rn(*a_ts, *b_ts);
+        const float scale = __fmul_rn(ld_after_wait(a_ts), ld_after_wait(b_ts));
         constexpr int ES = ODT == IF4_F32 ? 4 : 2;
         const uintptr_t al = reinterpret_cast<uintptr_t>(c) | (uintptr_t)((int64_t)N * ES);
         const int width = al % 32 == 0 ? 32 : al % 16 == 0 ? 16 : 0;
