@@ -330,6 +330,14 @@ __device__ __forceinline__ uint32_t absmax_f32(uint32_t a, float b)
     return r;
 }
 
+// max(|a|, |b|, |c|), NaN propagated
+__device__ __forceinline__ float absmax3_f32(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
 {
     uint32_t r;

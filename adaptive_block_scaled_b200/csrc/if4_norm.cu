@@ -321,92 +321,75 @@ __device__ __forceinline__ void load_h(const NormArgs &a, int64_t row, int g, Ra
 
 // Rows of up to G groups per thread of the block: one pass, h kept in
 // registers between the sum and the encode (the weight comes from L1 each
-// time).  A block takes rows blockIdx.x, + gridDim.x, ..., with the next S of
-// them under way in its threads' rings: 64 registers, 1024 threads per SM
-// whatever the block's size.
+// time).  A block takes rows blockIdx.x, + gridDim.x, ...; PREFETCH: the next
+// row's loads are issued as soon as h of a row is formed.
 //
-// Measured on IF4 8192 x 8192 bf16 with a residual, loads prefetched to
-// registers instead: one group per thread 92 us, two (128 registers, 512
-// threads per SM) 86-89 us.
-template <int DT, int G>
-struct NormRing {
-    static constexpr int S = DT != DT_F32 && G == 1 ? 2 : 1;     // rows under way
-    static constexpr int BYTES = S * 2 * G * 16 * elem_bytes<DT>();   // per thread: x, residual
-};
-
-template <int DT, int WT, int MODE, int G>
-__global__ void __launch_bounds__(1024, 1)
+// The encoder's and the norm's instructions bound it as much as memory does
+// (IF4 8192 x 8192 bf16: about 400 per group), so two groups per thread, which
+// share the row's sum, with loads straight to registers (128 of them, 512
+// threads per SM) beat one group (64 registers, 1024 threads: 92 us) and rows
+// under way in shared memory (85 us).
+template <int DT, int WT, int MODE, int G, bool PREFETCH>
+__global__ void __launch_bounds__(PREFETCH ? 512 : 1024, 1)
 rms_norm_quantize_rows_kernel(const __grid_constant__ NormArgs a)
 {
     pdl_enter();
-    using R = NormRing<DT, G>;
     __shared__ float inv_tab[128];
     __shared__ double sums[2][32];
-    extern __shared__ __align__(16) uint8_t norm_ring[];
     constexpr int GB = 16 * elem_bytes<DT>();
-    constexpr int GP = elem_bytes<DT>();                     // pieces of a group
     const float ts = ld_after_wait(a.ts);
     const float rts = __frcp_rn(ts);
     if (blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && a.err)
         atomicOr(a.err, IF4_DEV_BAD_SCALE);
     for (int i = threadIdx.x; i < 128; i += blockDim.x)
         inv_tab[i] = i == 0 ? 0.0f : __frcp_rn(__fmul_rn(f32_from_e4m3(i), ts));
-    // a warp's ring: [stage][x, residual][group of the lane][span of 32 groups]
-    constexpr uint32_t SPAN = 32 * GB;
-    const int g0 = threadIdx.x & ~31;              // the warp's first group
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(norm_ring) +
-                          (threadIdx.x >> 5) * (32 * R::BYTES);
-    auto fetch = [&](int64_t row, int stage) {
-        __syncwarp();                      // the lanes have read what this overwrites
-        if (row < a.rows) {
+    Raw<DT> x[PREFETCH ? G : 1], r[PREFETCH ? G : 1];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const int g = g0 + k * blockDim.x;
-                const uint32_t d = ring + (stage * 2 * G + k) * SPAN;
-                ring_copy<GP>(d, a.x + row * a.ld_x + (int64_t)g * GB, (a.gpr - g) * GP);
-                if (a.res)
-                    ring_copy<GP>(d + G * SPAN, a.res + row * a.ld_res + (int64_t)g * GB,
-                                  (a.gpr - g) * GP);
+        for (int k = 0; k < (PREFETCH ? G : 0); ++k) {
+            const int g = threadIdx.x + k * blockDim.x;
+            if (g < a.gpr) {
+                load_group_rw<DT>(a.x + row * a.ld_x + (int64_t)g * GB, x[k], a.v8);
+                if (a.res) load_group_rw<DT>(a.res + row * a.ld_res + (int64_t)g * GB, r[k], a.v8);
             }
         }
-        ring_commit();                     // also when empty: the waits count groups
     };
+#pragma unroll
+    for (int k = 0; k < (PREFETCH ? G : 0); ++k) {
+        zero_group(x[k]);
+        zero_group(r[k]);
+    }
     bool nonfinite = false;
     uint32_t top = 0;
-    int par = 0, stage = 0;
+    int par = 0;
     const int warps = blockDim.x >> 5;
     int64_t row = blockIdx.x;
-#pragma unroll
-    for (int i = 0; i < R::S; ++i) fetch(row + (int64_t)i * gridDim.x, i);
+    if (PREFETCH && row < a.rows) fetch(row);
     __syncthreads();                        // inv_tab
     for (; row < a.rows; row += gridDim.x, par ^= 1) {
-        ring_wait<R::S - 1>();
         double s = 0.0;
         Raw<DT> h[G];
 #pragma unroll
         for (int k = 0; k < G; ++k) {
-            zero_group(h[k]);
-            if (threadIdx.x + k * blockDim.x < a.gpr) {
-                const uint32_t d = ring + (stage * 2 * G + k) * SPAN;
-                ring_read<GP>(d, h[k].w);
-                if (a.res) {
-                    Raw<DT> r;
-                    ring_read<GP>(d + G * SPAN, r.w);
-                    add_residual<DT>(h[k], r);
-                }
+            if constexpr (PREFETCH) {
+                h[k] = x[k];
+                if (a.res) add_residual<DT>(h[k], r[k]);
+            } else {
+                const int g = threadIdx.x + k * blockDim.x;
+                zero_group(h[k]);
+                if (g < a.gpr) load_h<DT>(a, row, g, h[k]);
             }
             s = add_group_squares<DT>(s, h[k]);
         }
-        fetch(row + (int64_t)R::S * gridDim.x, stage);
-        if (++stage == R::S) stage = 0;
-        // h may be x's or the residual's memory: a warp stores only what it
-        // has copied itself, and no other warp reads that
+        // h may be x's or the residual's memory: this row's store only comes
+        // after this row's loads, and no other block reads this row
 #pragma unroll
         for (int k = 0; k < G; ++k) {
             const int g = threadIdx.x + k * blockDim.x;
             if (a.h && g < a.gpr)
                 store_group<DT>(a.h + row * a.ld_h + (int64_t)g * GB, h[k], a.v8);
         }
+        if (PREFETCH && row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (warps > 1) {
@@ -431,16 +414,15 @@ rms_norm_quantize_rows_kernel(const __grid_constant__ NormArgs a)
                 load_weight<WT>(a.w, g, w);
                 to_pairs<DT>(h[k], v);
                 to_pairs<WT>(w, wv);
-                uint32_t m0 = 0, m1 = 0;
+                float mx = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[j] = f2_mul(f2_mul(v[j], RS), wv[j]);
                     float lo, hi;
                     f2_unpack(v[j], lo, hi);
-                    m0 = absmax_f32(m0, lo);
-                    m1 = absmax_f32(m1, hi);
+                    mx = absmax3_f32(mx, lo, hi);
                 }
-                const uint32_t m = absmax_f32(m0, __uint_as_float(m1)) & 0x7FFFFFFFu;
+                const uint32_t m = __float_as_uint(mx);
                 nonfinite |= m >= 0x7F800000u;
                 top = max(top, m);
                 const GroupCode c = encode_registers<MODE>(v, __uint_as_float(m), ts, rts, inv_tab);
@@ -938,19 +920,23 @@ int rms_norm_quantize_entry(const void *x, int64_t ld_x, const void *res, int64_
     return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
         constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
         const int64_t warps = (n + 31) / 32;
-        auto rows_kernel = [&](auto G) {
-            constexpr int g = decltype(G)::value;
+        auto rows_kernel = [&](auto k, int g, unsigned per_sm) {
             // the fewest whole warps that hold a row; blocks for one wave
             const unsigned threads = (unsigned)((warps + g - 1) / g * 32);
-            const unsigned per_sm = std::min<unsigned>(1024 / threads, 32);
-            return launch_rows(rms_norm_quantize_rows_kernel<DT, WT, MODE, g>,
-                               (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * per_sm),
-                               threads, threads * NormRing<DT, g>::BYTES,
-                               1024 * NormRing<DT, g>::BYTES, d, st, a);
+            const int64_t wave = (int64_t)d.sm_count * std::min<unsigned>(per_sm / threads, 32);
+            return launch_k(k, (unsigned)std::min(rows, wave), threads, st, a);
         };
-        if (n <= 1024) return rows_kernel(std::integral_constant<int, 1>{});
-        if constexpr (DT != DT_F32)
-            if (n <= 2048) return rows_kernel(std::integral_constant<int, 2>{});
+        if constexpr (DT == DT_F32) {
+            if (n <= 1024)
+                return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 1, false>, 1, 1024);
+        } else {
+            if (n <= 32)
+                return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 1, false>, 1, 1024);
+            if (n <= 1024)
+                return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 2, true>, 2, 512);
+            if (n <= 2048)
+                return rows_kernel(rms_norm_quantize_rows_kernel<DT, WT, MODE, 2, false>, 2, 1024);
+        }
         return launch_k(rms_norm_quantize_kernel<DT, WT, MODE>,
                         (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8),
                         (unsigned)NORM_THREADS, st, a);
