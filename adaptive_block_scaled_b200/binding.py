@@ -123,12 +123,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream):
     if stream is None:
-        return _vp(_raw_stream(torch.cuda.current_device()))
-    return _vp(stream.cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return _vp(t.data_ptr()) if t is not None else _vp(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _matrix(t, name):
@@ -146,7 +146,7 @@ def _dtype(t, name):
 
 
 def _u8(t, name, shape):
-    if t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {tuple(shape)}")
 
 
@@ -401,10 +401,6 @@ def _call(name, dev, stream, *args):
         _check(rc, name)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 def _new(rows, cols, dtype, device):
     # empty_strided: 1.5 us per call against torch.empty's 2.5
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
@@ -460,7 +456,7 @@ def _nvfp4_linear(a, b, ws, c, err_flag, stream):
     wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     _call("nvfp4_linear", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), a_ts.data_ptr(),
           b_codes.data_ptr(), b_scales.data_ptr(), b_ts.data_ptr(), M, N, 2 * kb, wp, wn,
-          c.data_ptr(), _dtype(c, "c"), _at(err_flag))
+          c.data_ptr(), _dtype(c, "c"), _ptr(err_flag))
 
 
 def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, err_flag,
@@ -500,9 +496,9 @@ def _quantize_t(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_fla
     rows, cols = x.shape
     _word(ts, "ts", torch.float32)
     _word(err_flag, "err_flag", torch.int32)
-    _call(entry, dev, stream, x.data_ptr(), _dtype(x, "x"), rows, cols, ld, _at(codes),
-          _at(scales), codes_t.data_ptr(), scales_t.data_ptr(), ts.data_ptr(), ts_mode,
-          _at(err_flag))
+    _call(entry, dev, stream, x.data_ptr(), _dtype(x, "x"), rows, cols, ld, _ptr(codes),
+          _ptr(scales), codes_t.data_ptr(), scales_t.data_ptr(), ts.data_ptr(), ts_mode,
+          _ptr(err_flag))
 
 
 def _quantize_t_into(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream):
@@ -575,9 +571,9 @@ def _rms_norm(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax,
     _word(ts, "ts", torch.float32)
     _word(amax, "amax", torch.float32)
     _word(err_flag, "err_flag", torch.int32)
-    _call(entry, dev, stream, x.data_ptr(), ld, _at(residual), ld_res, weight.data_ptr(),
-          _dtype(weight, "weight"), _dtype(x, "x"), rows, cols, eps, _at(h), ld_h, _at(rstd),
-          codes.data_ptr(), scales.data_ptr(), ts.data_ptr(), _at(amax), _at(err_flag))
+    _call(entry, dev, stream, x.data_ptr(), ld, _ptr(residual), ld_res, weight.data_ptr(),
+          _dtype(weight, "weight"), _dtype(x, "x"), rows, cols, eps, _ptr(h), ld_h, _ptr(rstd),
+          codes.data_ptr(), scales.data_ptr(), ts.data_ptr(), _ptr(amax), _ptr(err_flag))
 
 
 def _rms_norm_into(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag,
@@ -641,7 +637,7 @@ def if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, workspace, str
     wp, wn = ((None, 0) if workspace is None else
               (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     _call(name, dev, stream, dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(),
-          _dtype(weight, "weight"), rstd.data_ptr(), _at(dres), ld_dres, _dtype(h, "h"), rows, cols,
+          _dtype(weight, "weight"), rstd.data_ptr(), _ptr(dres), ld_dres, _dtype(h, "h"), rows, cols,
           dx.data_ptr(), ld_dx, dweight.data_ptr(), wp, wn)
 
 
@@ -836,7 +832,7 @@ def quantize_fused(x, with_nvfp4=True, sync_words=None, err_flag=None, stream=No
 
 def dequantize(codes, scales, ts, dtype=torch.bfloat16, stream=None):
     rows, cols = codes.shape[0], codes.shape[1] * 2
-    y = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    y = _new(rows, cols, dtype, codes.device)
     if4_dequantize(codes, scales, ts, y, stream)
     return y
 
