@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -45,6 +46,22 @@ int check_device(DeviceInfo &d)
 {
     if (!device_info(d)) return IF4_ERR_CUDA;
     if (d.cc_major != 10) return IF4_ERR_DEVICE;
+    return IF4_OK;
+}
+
+// Raises a kernel's dynamic shared-memory limit, once per device (a race only
+// repeats the call; nothing here throws).
+typedef std::atomic<bool> OncePerDevice[MAX_DEVICES];
+
+template <typename Kernel>
+int allow_smem(Kernel kernel, int bytes, const DeviceInfo &d, OncePerDevice &done)
+{
+    if (!done[d.id].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess)
+            return IF4_ERR_CUDA;
+        done[d.id].store(true, std::memory_order_release);
+    }
     return IF4_OK;
 }
 

@@ -21,9 +21,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "../../include/if4.h"
 #include "if4_device.cuh"
@@ -512,6 +509,7 @@ rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
 // -------------------------------------------------------------- gradient ----
 
 constexpr int BACK_BLOCKS = 296;     // blocks that share the rows, and partial sums of dw
+constexpr int MAX_BACK_SMEM = 226 * 1024;   // a block's limit less its static arrays
 
 struct BackArgs {
     const char *dy, *h, *w, *dres;
@@ -856,38 +854,6 @@ int by_types(int x_dtype, int w_dtype, F f)
     return w_dtype == IF4_F32 ? f(HF{}, F32{}) : f(HF{}, HF{});
 }
 
-// Programmatic launch with dynamic shared memory (at most `most` bytes, allowed
-// once per kernel and device).
-template <typename... KArgs, typename... Args>
-int launch_rows(void (*kernel)(KArgs...), unsigned grid, unsigned threads, unsigned smem,
-                unsigned most, const DeviceInfo &d, cudaStream_t st, Args... args)
-{
-    if (smem > 48 * 1024) {
-        static std::mutex mu;
-        static std::set<std::pair<const void *, int>> allowed;
-        std::lock_guard<std::mutex> lock(mu);
-        const auto key = std::make_pair(reinterpret_cast<const void *>(kernel), d.id);
-        if (!allowed.count(key)) {
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)most) != cudaSuccess)
-                return IF4_ERR_CUDA;
-            allowed.insert(key);
-        }
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return IF4_ERR_CUDA;
-    return launch_status();
-}
-
 template <int MODE>
 int rms_norm_quantize_entry(const void *x, int64_t ld_x, const void *res, int64_t ld_res,
                             const void *w, int w_dtype, int x_dtype, int64_t rows, int64_t cols,
@@ -1026,10 +992,24 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
                                                      units > 512 ? BACK_BLOCKS / 2 : BACK_BLOCKS);
             auto rows_kernel = [&](auto V) {
                 constexpr int U = decltype(V)::value;
-                const unsigned smem = threads * BackRing<DT, U>::BYTES +
-                                      (unsigned)((slots - 1) * cols * sizeof(float));
-                return launch_rows(rms_norm_backward_rows_kernel<DT, WT, U>, (unsigned)parts,
-                                   (unsigned)threads, smem, 227u * 1024u - 512u, d, st, a, T);
+                auto kernel = rms_norm_backward_rows_kernel<DT, WT, U>;
+                static OncePerDevice done;
+                const int ok = allow_smem(kernel, MAX_BACK_SMEM, d, done);
+                if (ok != IF4_OK) return ok;
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3((unsigned)parts, 1, 1);
+                cfg.blockDim = dim3((unsigned)threads, 1, 1);
+                cfg.dynamicSmemBytes = (size_t)threads * BackRing<DT, U>::BYTES +
+                                       (size_t)(slots - 1) * (size_t)cols * sizeof(float);
+                cfg.stream = st;
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+                attr[0].val.programmaticStreamSerializationAllowed = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                if (cudaLaunchKernelEx(&cfg, kernel, a, T) != cudaSuccess)
+                    return (int)IF4_ERR_CUDA;
+                return launch_status();
             };
             int r;
             if constexpr (DT != DT_F32)

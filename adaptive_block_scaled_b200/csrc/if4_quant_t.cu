@@ -207,12 +207,9 @@ int launch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t cols,
 {
     auto kernel = quantize_t_kernel<DT, MODE, ROWS>;
     constexpr int SMEM = smem_t_bytes<DT>();
-    static std::once_flag once[MAX_DEVICES];
-    static cudaError_t rcs[MAX_DEVICES];
-    std::call_once(once[d.id], [&] {
-        rcs[d.id] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    });
-    if (rcs[d.id] != cudaSuccess) return IF4_ERR_CUDA;
+    static OncePerDevice done;
+    const int rc = allow_smem(kernel, SMEM, d, done);
+    if (rc != IF4_OK) return rc;
     const int64_t tiles = ((rows + TILE - 1) / TILE) * ((cols + TILE - 1) / TILE);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tiles, 1, 1);

@@ -24,7 +24,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <mutex>
 
 #include "../../include/if4.h"
 #include "if4_device.cuh"
@@ -913,25 +912,13 @@ struct Problem {
     cudaStream_t st;
 };
 
-// The kernel's shared-memory limit is raised once per device and kernel.
-template <typename Kernel>
-int allow_smem(Kernel kernel, int bytes, const DeviceInfo &d, std::once_flag (&once)[MAX_DEVICES],
-               cudaError_t (&rcs)[MAX_DEVICES])
-{
-    std::call_once(once[d.id], [&] {
-        rcs[d.id] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    });
-    return rcs[d.id] == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
-}
-
 template <int NT, int VEC, int ODT>
 int launch_split(const Problem &p, const DeviceInfo &d, int ranks)
 {
     using C = split::Cfg<NT>;
     auto kernel = nvfp4_linear_split<NT, VEC, ODT>;
-    static std::once_flag once[MAX_DEVICES];
-    static cudaError_t rcs[MAX_DEVICES];
-    const int rc = allow_smem(kernel, C::SMEM, d, once, rcs);
+    static OncePerDevice done;
+    const int rc = allow_smem(kernel, C::SMEM, d, done);
     if (rc != IF4_OK) return rc;
     CUtensorMap mw, mx;
     if (!make_codes_map(&mw, p.b_codes, p.N, p.K, split::WR) ||
@@ -1003,10 +990,9 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
 {
     using C = duo::Cfg<BN>;
     auto kernel = nvfp4_linear_pair<BN, ODT>;
-    static std::once_flag once[MAX_DEVICES], occ_once[MAX_DEVICES];
-    static cudaError_t rcs[MAX_DEVICES];
-    static int resident[MAX_DEVICES];
-    const int rc = allow_smem(kernel, C::SMEM, d, once, rcs);
+    static OncePerDevice done;
+    static std::atomic<int> resident[MAX_DEVICES];
+    const int rc = allow_smem(kernel, C::SMEM, d, done);
     if (rc != IF4_OK) return rc;
     ScalePack sa{p.a_scales, static_cast<uint8_t *>(p.workspace), (int)p.M, 2 * duo::PM, 2};
     ScalePack sb{p.b_scales, nullptr, (int)p.N, BN, C::SFB_BLOCKS};
@@ -1043,17 +1029,18 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
     cfg.numAttrs = 2;
     // persistent: as many pairs as can be resident at once (the SMs of a pair
     // share a GPC, so this can be below sms / 2)
-    std::call_once(occ_once[d.id], [&] {
+    int pairs_max = resident[d.id].load(std::memory_order_relaxed);
+    if (pairs_max == 0) {
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
-            resident[d.id] = n;
-        else
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
             (void)cudaGetLastError();
-    });
+            n = 0;
+        }
+        pairs_max = n > 0 && n < d.sm_count / 2 ? n : d.sm_count / 2;
+        resident[d.id].store(pairs_max, std::memory_order_relaxed);
+    }
     const int64_t tiles = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + BN - 1) / BN);
-    int64_t pairs = resident[d.id] > 0 ? resident[d.id] : d.sm_count / 2;
-    if (pairs > d.sm_count / 2) pairs = d.sm_count / 2;
-    if (tiles < pairs) pairs = tiles;
+    const int64_t pairs = tiles < pairs_max ? tiles : pairs_max;
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
     if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mc, boxes ? 1 : 0, p.a_ts, p.b_ts, p.c, (int)p.M, (int)p.N,
                            (int)p.K, p.err) != cudaSuccess)
