@@ -131,6 +131,20 @@ __device__ __forceinline__ void load_scales16(const uint8_t *p, int nb, uint32_t
         for (int j = 0; j < 4; ++j)
             if (nb > 4 * j)
                 asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[j]) : "l"(p + 4 * j));
+    } else if (nb >= 16) {
+        // rows on 4-byte and on 2-byte boundaries in turn: the aligned words
+        // that hold the 16 bytes (the first may begin in the row before), the
+        // last two bytes by themselves, shifted together
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 2u;
+        uint32_t a[5];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(a[j]) : "l"(p - off + 4 * j));
+        uint16_t last = 0;
+        if (off) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(last) : "l"(p + 14));
+        a[4] = last;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(a[j], a[j + 1], 8 * off);
     } else {
         uint16_t h[8];
 #pragma unroll
@@ -155,6 +169,155 @@ __device__ __forceinline__ void store_c(void *c, int64_t i, float v)
     } else {
         static_cast<__half *>(c)[i] = __float2half_rn(v);
     }
+}
+
+// --------------------------------------------------- one or two tokens ----
+//
+// A warp computes ROWS output columns for all tokens.  Its lanes take pieces
+// of 32 along K (16 code bytes, 2 scale bytes) in turn.  Codes become f16x2
+// values by conversion; the 8 products of each half of a group are multiples
+// of 1/4 of at most 36, so their sum in f16 (at most 288, 11 bits) is exact;
+// the product of the two scales (8 bits) and its product with the group's sum
+// (20 bits) are exact in binary32, which takes one rounding per group.
+//
+// Nothing here waits for anything but the loads: no tensor memory, barrier
+// or cluster stands between the launch and them.  A token of 4096 x 4096 takes
+// 3.0 us (5.7 with the kernel below; the weight's bytes are 1.5), two tokens
+// 4.2 (5.8).  The conversions bound it: four tokens take 7.3 us (5.8), and a
+// token of 16384 x 4096 11.1 (10.0).  Two columns per warp and eight warps per
+// block, all loads of a chunk up front: four columns took 4.5 us, one 3.7, four
+// warps 3.4.
+
+namespace few {
+
+constexpr int ROWS = 2;                        // output columns per warp
+constexpr int CHUNK = 4;                       // pieces per lane under way
+constexpr int WARPS = 8;
+
+// Sizes it is faster for than the split kernel (us here / there, one token
+// unless said otherwise): 8192 x 4096 4.8 / 6.2, 4096 x 8192 6.3 / 6.4, two of 4096 x
+// 4096 4.2 / 5.7; but two of 8192 x 4096 7.2 / 6.2, 16384 x 4096 11.1 / 10.0,
+// 14336 x 2048 7.1 / 6.2 and 2048 x 14336 9.4 / 6.9.
+inline bool takes(int64_t M, int64_t N, int64_t K)
+{
+    return M <= 2 && N <= 8192 && K <= 8192 && M * N * K <= (1 << 25);
+}
+
+}  // namespace few
+
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t word, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(word));
+}
+
+// Two scale bytes as floats (bit 7 is reported elsewhere).
+__device__ __forceinline__ void e4m3x2_to_f32(uint32_t two, float (&s)[2])
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    s[0] = f16lo_to_f32(h);
+    s[1] = f16hi_to_f32(h);
+}
+
+template <int MT, int ODT>
+__global__ void __launch_bounds__(few::WARPS * 32)
+nvfp4_linear_few(const uint8_t *x_codes, const uint8_t *x_scales, const float *x_ts,
+                 const uint8_t *w_codes, const uint8_t *w_scales, const float *w_ts, void *c, int M,
+                 int N, int K, int *err)
+{
+    using namespace few;
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const int n0 = (blockIdx.x * WARPS + (threadIdx.x >> 5)) * ROWS;
+    if (n0 >= N) return;
+    const int pieces = K / 32;
+    const int64_t cb = K / 2, sb = K / 16;         // bytes of a row
+    float acc[ROWS][MT];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] = 0.0f;
+    uint32_t bad = 0;
+    auto load = [&](const uint8_t *codes, const uint8_t *scales, int64_t row, int piece, bool in,
+                    uint32_t (&w)[4], uint32_t &s) {
+        w[0] = w[1] = w[2] = w[3] = s = 0u;
+        if (in) {
+            asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "l"(codes + row * cb + (int64_t)piece * 16));
+            uint16_t h;
+            asm volatile("ld.global.nc.u16 %0, [%1];"
+                         : "=h"(h) : "l"(scales + row * sb + (int64_t)piece * 2));
+            s = h;
+        }
+    };
+    for (int p0 = lane; p0 < pieces; p0 += 32 * CHUNK) {
+        uint32_t w[CHUNK][ROWS][4], ws[CHUNK][ROWS], x[CHUNK][MT][4], xsc[CHUNK][MT];
+#pragma unroll
+        for (int q = 0; q < CHUNK; ++q)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                load(x_codes, x_scales, m, p0 + 32 * q, p0 + 32 * q < pieces && m < M, x[q][m],
+                     xsc[q][m]);
+#pragma unroll
+        for (int q = 0; q < CHUNK; ++q)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                load(w_codes, w_scales, n0 + r, p0 + 32 * q,
+                     p0 + 32 * q < pieces && n0 + r < N, w[q][r], ws[q][r]);
+#pragma unroll
+        for (int q = 0; q < CHUNK; ++q) {
+            uint32_t xh[MT][4][4];
+            float xs[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e2m1x8_to_f16(x[q][m][j], xh[m][j]);
+                e4m3x2_to_f32(xsc[q][m], xs[m]);
+                bad |= xsc[q][m];
+            }
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                uint32_t wh[4][4];
+                float sw[2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e2m1x8_to_f16(w[q][r][j], wh[j]);
+                e4m3x2_to_f32(ws[q][r], sw);
+                bad |= ws[q][r];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t d = 0u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            asm("fma.rn.f16x2 %0, %1, %2, %0;"
+                                : "+r"(d) : "r"(wh[2 * g + j / 4][j % 4]),
+                                  "r"(xh[m][2 * g + j / 4][j % 4]));
+                        const float dot = __fadd_rn(f16lo_to_f32(d), f16hi_to_f32(d));
+                        acc[r][m] = __fmaf_rn(dot, __fmul_rn(sw[g], xs[m][g]), acc[r][m]);
+                    }
+            }
+        }
+    }
+    const float scale = __fmul_rn(ld_after_wait(x_ts), ld_after_wait(w_ts));
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float v = acc[r][m];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+            if (lane == r * MT + m && m < M && n0 + r < N)
+                store_c<ODT>(c, (int64_t)m * N + n0 + r, __fmul_rn(v, scale));
+        }
+    if ((bad & 0x8080u) && err) atomicOr(err, IF4_DEV_BAD_SCALE);
 }
 
 // ------------------------------------------------- few rows: split over K ----
@@ -912,6 +1075,15 @@ struct Problem {
     cudaStream_t st;
 };
 
+template <int MT, int ODT>
+int launch_few(const Problem &p)
+{
+    const int64_t per_block = few::WARPS * few::ROWS;
+    return launch_k(nvfp4_linear_few<MT, ODT>, (unsigned)((p.N + per_block - 1) / per_block),
+                    (unsigned)few::WARPS * 32u, p.st, p.a_codes, p.a_scales, p.a_ts, p.b_codes,
+                    p.b_scales, p.b_ts, p.c, (int)p.M, (int)p.N, (int)p.K, p.err);
+}
+
 template <int NT, int VEC, int ODT>
 int launch_split(const Problem &p, const DeviceInfo &d, int ranks)
 {
@@ -1057,6 +1229,8 @@ int launch_linear(const Problem &p, const DeviceInfo &d)
         return narrow <= d.sm_count / 2 ? launch_pair<128, VEC, ODT>(p, d)
                                         : launch_pair<240, VEC, ODT>(p, d);
     }
+    if (few::takes(p.M, p.N, p.K))
+        return p.M == 1 ? launch_few<1, ODT>(p) : launch_few<2, ODT>(p);
     // As few tokens per CTA as leave each output tile an SM of its own (32
     // tokens of 4096 x 4096: 16 per CTA 6.5 us, 32 per CTA 7.2), and the
     // largest power of two of K ranks that still runs in one wave (a second

@@ -65,7 +65,12 @@ def cuda(t):
 SIZES = [(1, 1, 32), (1, 16, 32), (3, 7, 96), (1, 4096, 4096), (16, 128, 256), (17, 130, 288),
          (33, 300, 4128), (64, 129, 544), (65, 257, 1056), (128, 640, 2048), (5, 1000, 8192),
          (129, 129, 64), (256, 256, 512), (257, 513, 800), (1001, 1555, 4128), (2048, 2304, 1024),
-         (300, 128, 512), (1300, 60, 320), (700, 20000, 96), (130, 264, 16384)]
+         (300, 128, 512), (1300, 60, 320), (700, 20000, 96), (130, 264, 16384),
+         # one and two tokens: whole and partial chunks of K, odd columns, and
+         # sizes past the few-token kernel's
+         (1, 37, 4128), (2, 129, 1056), (2, 4096, 4096), (1, 8193, 64), (2, 16, 8224),
+         # one tile more and fewer than the pairs of SMs
+         (256, 128 * 74, 64), (256, 128 * 75, 64), (512, 241, 544)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
@@ -103,7 +108,7 @@ def test_operands_from_every_nvfp4_quantizer(M, N):
         check(bb.linear_nvfp4(a, b, torch.float32), a[:2], b[:2], a[2], b[2])
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 130, 512), (140, 300, 768)])
+@pytest.mark.parametrize("M,N,K", [(2, 130, 512), (4, 130, 512), (140, 300, 768)])
 def test_all_scales_and_signed_zeros(M, N, K):
     """Every finite E4M3 scale byte, zero included, and every code."""
     g = torch.Generator().manual_seed(K)
@@ -114,21 +119,22 @@ def test_all_scales_and_signed_zeros(M, N, K):
     check(c, a, b, one, one)
 
 
-@pytest.mark.parametrize("M,N", [(8, 256), (256, 256)])
+@pytest.mark.parametrize("M,N", [(2, 256), (8, 256), (256, 256)])
 def test_nan_scale_stays_in_its_row_and_column(M, N):
     g = torch.Generator().manual_seed(9)
     a, b = operand(M, 512, g), operand(N, 512, g)
-    a[1][3, 7] = 0x7F
+    a[1][1, 7] = 0x7F
     b[1][11, 31] = 0x7F
     one = torch.ones(1, device="cuda")
     c, err = run(cuda(a), cuda(b), one, one, torch.float32)
     assert int(err) == 0
     want = torch.zeros((M, N), dtype=torch.bool)
-    want[3], want[:, 11] = True, True
+    want[1], want[:, 11] = True, True
     assert torch.equal(c.isnan().cpu(), want)
 
 
-@pytest.mark.parametrize("M,N,K", [(8, 256, 256), (8, 256, 288), (256, 256, 256), (256, 256, 288)])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 256), (2, 33, 288), (8, 256, 256), (8, 256, 288),
+                                   (256, 256, 256), (256, 256, 288)])
 @pytest.mark.parametrize("which", [0, 1])
 def test_int4_groups_are_reported(M, N, K, which):
     g = torch.Generator().manual_seed(9)
@@ -139,7 +145,7 @@ def test_int4_groups_are_reported(M, N, K, which):
     assert int(err) == B().DEV_BAD_SCALE
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 200, 512), (130, 200, 512), (130, 201, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 201, 512), (3, 200, 512), (130, 200, 512), (130, 201, 512)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_alignment_and_no_writes_outside(M, N, K, dtype):
     """Scales on a 4-byte boundary only, codes on 16, C on its element's."""
