@@ -42,6 +42,30 @@ __device__ __forceinline__ void load_group(const char *p, Raw<DT> &r)
     }
 }
 
+// The same for values that an earlier kernel of the stream may have written, or
+// that this kernel overwrites itself: coherent, and not moved in front of
+// pdl_enter().  v8: 32-byte aligned, 256 bits at once.
+template <int DT>
+__device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r, bool v8)
+{
+    if (v8) {
+#pragma unroll
+        for (int q = 0; q < (DT == DT_F32 ? 2 : 1); ++q)
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(r.w[8 * q]), "=r"(r.w[8 * q + 1]), "=r"(r.w[8 * q + 2]),
+                           "=r"(r.w[8 * q + 3]), "=r"(r.w[8 * q + 4]), "=r"(r.w[8 * q + 5]),
+                           "=r"(r.w[8 * q + 6]), "=r"(r.w[8 * q + 7])
+                         : "l"(p + 32 * q));
+    } else {
+#pragma unroll
+        for (int q = 0; q < (DT == DT_F32 ? 4 : 2); ++q)
+            asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]),
+                           "=r"(r.w[4 * q + 3])
+                         : "l"(p + 16 * q));
+    }
+}
+
 // Unpack to 8 float pairs (element 2j low, 2j+1 high) and the group's max |x|
 // as float bits; *nonfinite is set for Inf/NaN.
 template <int DT>
@@ -113,6 +137,17 @@ __device__ __forceinline__ GroupCode encode_registers(const f2_t (&x)[8], float 
         if (sb == 0) out.c0 = out.c1 = out.scale = 0u;
         return out;
     }
+}
+
+// ts = amax / 2688, 1 for amax == 0, floored at 2^-117 (NaN stays NaN).
+__device__ __forceinline__ float tensor_scale_of(float a)
+{
+    float t = 1.0f;
+    if (a != 0.0f) {
+        t = __fdiv_rn(a, 2688.0f);
+        if (t < kTsFloor) t = kTsFloor;
+    }
+    return t;
 }
 
 // inv_tab of encode_registers, by threads 0..127 of a block (no barrier).

@@ -72,17 +72,6 @@ __device__ __forceinline__ void store_group(char *p, const Raw<DT> &r)
         st_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
 }
 
-template <int DT>
-__device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r)
-{
-#pragma unroll
-    for (int q = 0; q < (DT == DT_F32 ? 4 : 2); ++q)
-        asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]),
-                       "=r"(r.w[4 * q + 3])
-                     : "l"(p + 16 * q));
-}
-
 // Sum over a block of NORM_THREADS; every thread gets it.
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T *buf)
@@ -148,25 +137,7 @@ __device__ __forceinline__ float row_rstd(double s, double inv_cols, double eps)
     return (float)r;
 }
 
-// 256-bit (32-byte aligned addresses) or 128-bit coherent loads and stores of
-// one group, past L1: h may be x's or the residual's own memory, so these are
-// not read through the read-only path.
-template <int DT>
-__device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r, bool v8)
-{
-    if (v8) {
-#pragma unroll
-        for (int q = 0; q < (DT == DT_F32 ? 2 : 1); ++q)
-            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                         : "=r"(r.w[8 * q]), "=r"(r.w[8 * q + 1]), "=r"(r.w[8 * q + 2]),
-                           "=r"(r.w[8 * q + 3]), "=r"(r.w[8 * q + 4]), "=r"(r.w[8 * q + 5]),
-                           "=r"(r.w[8 * q + 6]), "=r"(r.w[8 * q + 7])
-                         : "l"(p + 32 * q));
-    } else {
-        load_group_rw<DT>(p, r);
-    }
-}
-
+// The same for stores, 256 bits where the addresses allow it.
 template <int DT>
 __device__ __forceinline__ void store_group(char *p, const Raw<DT> &r, bool v8)
 {
@@ -743,8 +714,8 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
             Raw<DT> hr, dr;
             Raw<WT> wr;
             f2_t h[8], d[8], w[8];
-            load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr);
-            load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr);
+            load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr, a.v8);
+            load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr, a.v8);
             load_weight<WT>(a.w, g, wr);
             to_pairs<DT>(hr, h);
             to_pairs<DT>(dr, d);
@@ -764,14 +735,14 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
             Raw<DT> hr, dr, er;
             Raw<WT> wr;
             f2_t h[8], d[8], w[8], e[8];
-            load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr);
-            load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr);
+            load_group_rw<DT>(a.h + row * a.ld_h + (int64_t)g * GB, hr, a.v8);
+            load_group_rw<DT>(a.dy + row * a.ld_dy + (int64_t)g * GB, dr, a.v8);
             load_weight<WT>(a.w, g, wr);
             to_pairs<DT>(hr, h);
             to_pairs<DT>(dr, d);
             to_pairs<WT>(wr, w);
             if (a.dres) {
-                load_group_rw<DT>(a.dres + row * a.ld_dres + (int64_t)g * GB, er);
+                load_group_rw<DT>(a.dres + row * a.ld_dres + (int64_t)g * GB, er, a.v8);
                 to_pairs<DT>(er, e);
             }
 #pragma unroll

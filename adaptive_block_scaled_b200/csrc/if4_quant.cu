@@ -685,17 +685,6 @@ amax_kernel(const char *__restrict__ x, int64_t ld_bytes, uint32_t gpr, uint32_t
     }
 }
 
-// ts = amax / 2688, 1 for amax == 0, floored at 2^-117 (NaN stays NaN).
-__device__ __forceinline__ float tensor_scale_of(float a)
-{
-    float t = 1.0f;
-    if (a != 0.0f) {
-        t = __fdiv_rn(a, 2688.0f);
-        if (t < kTsFloor) t = kTsFloor;
-    }
-    return t;
-}
-
 __global__ void tensor_scale_kernel(const float *amax, float *ts)
 {
     pdl_enter();

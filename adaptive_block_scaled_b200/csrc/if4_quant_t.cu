@@ -9,19 +9,20 @@
 //   dW = dY^T X   contracts over M: dY^T and X^T grouped along M,
 // so each of X, W and dY is needed both ways.
 //
-// A block takes a tile of 128 x 128 into shared memory with asynchronous
-// 16-byte copies, which hold no registers while they are under way.  Row form:
-// a thread reads whole row groups (16 values, 32 or 64 bytes) and encodes them.
+// A block takes a tile of 128 x 128 (64 x 64 for small tensors) into shared
+// memory with asynchronous 16-byte copies, which hold no registers while they
+// are under way.  Row form: a thread reads whole row groups (16 values, 32 or 64 bytes) and encodes them.
 // Column form: a thread reads 16 rows of two neighbouring columns (one
 // conflict-free word per row), which are two whole column groups in registers,
 // and encodes them with the same group encoder.  The column codes are put back
-// in order through shared memory, so that the tile's 64 code bytes of a column
-// leave as one run.
+// in order through shared memory, so that a tile's code bytes of a column leave
+// as one run.
 //
 // With both forms and IF4 the encoder's instructions bound it (two encodes of
-// about 200 instructions per 16 values; 8192 x 8192 bf16, tensor scale given);
-// four blocks per SM keep 32 warps issuing.  Holding the tile's loads in
-// registers instead allowed two: 83 us.
+// about 200 instructions per 16 values, 270 in all): 8192 x 8192 bf16 with the
+// tensor scale given takes 76 us, four blocks per SM issuing in 82 % of the
+// cycles.  Holding the tile's loads in registers instead allowed two: 83 us.
+// NVFP4 takes 49 us (155 instructions).
 
 #include <cuda_runtime.h>
 
@@ -36,21 +37,86 @@
 
 namespace {
 
-constexpr int TILE = 128;                 // rows and columns of a block's tile
-constexpr int TG = TILE / 16;             // groups along one side
-constexpr int CODE_PITCH = TILE / 2 + 8;  // staged code bytes per column
 constexpr int THREADS_T = 256;
 
+// A block's tile of T x T.
+template <int DT, int T>
+struct Tile {
+    static constexpr int PITCH = T * (DT == DT_F32 ? 4 : 2);     // bytes of a row
+    static constexpr int GROUPS = T / 16;                        // along one side
+    static constexpr int CODE_PITCH = T / 2 + 8;                 // staged code bytes per column
+    static constexpr int CODE_OFF = T * PITCH;
+    static constexpr int SCALE_OFF = CODE_OFF + T * CODE_PITCH;
+    static constexpr int SMEM = SCALE_OFF + T * GROUPS;
+};
+
+// Tensor scale, first step: block i's max |x| as float bits to parts[i] (NaN and
+// Inf compare above every finite value).  A float per block needs no zeroed
+// word and no atomics; the parts lie in the column codes' own memory, which the
+// quantizer writes only after the second step has read them.
 template <int DT>
-__host__ __device__ constexpr int tile_bytes()
+__global__ void __launch_bounds__(256)
+amax_parts_kernel(const char *x, int64_t ld_bytes, uint32_t gpr, uint32_t ngroups, bool v8,
+                  uint32_t *parts)
 {
-    return TILE * TILE * elem_bytes<DT>();
+    pdl_enter();
+    constexpr int U = DT == DT_F32 ? 4 : 8;       // loads in flight
+    const uint32_t stride = gridDim.x * blockDim.x;
+    uint32_t m = 0;
+    for (uint64_t g0 = blockIdx.x * blockDim.x + threadIdx.x; g0 < ngroups;
+         g0 += (uint64_t)U * stride) {
+        Raw<DT> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint64_t g = g0 + (uint64_t)u * stride;
+            if (g < ngroups) {
+                const uint32_t row = (uint32_t)g / gpr;
+                load_group_rw<DT>(x + (int64_t)row * ld_bytes +
+                                      (int64_t)((uint32_t)g - row * gpr) * 16 * elem_bytes<DT>(),
+                                  r[u], v8);
+            } else {
+#pragma unroll
+                for (uint32_t &w : r[u].w) w = 0u;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            f2_t xv[8];
+            bool bad;
+            m = max(m, __float_as_uint(unpack_group<DT>(r[u], xv, bad)));
+        }
+    }
+    __shared__ uint32_t warp_max[8];
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, warp_max[i]);
+        parts[blockIdx.x] = m;
+    }
 }
 
-template <int DT>
-__host__ __device__ constexpr int smem_t_bytes()
+// Second step: ts of n parts, by one block.
+__global__ void __launch_bounds__(256)
+scale_parts_kernel(const uint32_t *parts, int n, float *ts)
 {
-    return tile_bytes<DT>() + TILE * CODE_PITCH + TILE * TG;
+    pdl_enter();
+    __shared__ uint32_t warp_max[8];
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < n; i += 256) {
+        uint32_t v;
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(parts + i) : "memory");
+        m = max(m, v);
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, warp_max[i]);
+        *ts = tensor_scale_of(__uint_as_float(m));
+    }
 }
 
 // Byte offset of 16-byte piece k of a tile row.  The pieces are permuted inside
@@ -69,7 +135,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool i
                  :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-template <int DT, int MODE, bool ROWS>
+template <int DT, int MODE, bool ROWS, int T>
 __global__ void __launch_bounds__(THREADS_T, DT == DT_F32 ? 2 : 4)
 quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, int64_t cols,
                   uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
@@ -78,13 +144,14 @@ quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, in
 {
     pdl_enter();
     constexpr int ES = elem_bytes<DT>();
-    constexpr int PITCH = TILE * ES;
+    using L = Tile<DT, T>;
+    constexpr int TILE = T, TG = L::GROUPS, CODE_PITCH = L::CODE_PITCH, PITCH = L::PITCH;
     constexpr int PIECES = PITCH / 16;      // 16-byte pieces of a tile row
     constexpr int GP = ES;                  // pieces of a group: 2 or 4
     extern __shared__ __align__(16) uint8_t smem_t[];
     uint8_t *tile = smem_t;
-    uint8_t *code_out = smem_t + tile_bytes<DT>();
-    uint8_t *scale_out = code_out + TILE * CODE_PITCH;
+    uint8_t *code_out = smem_t + L::CODE_OFF;
+    uint8_t *scale_out = smem_t + L::SCALE_OFF;
     __shared__ float inv_tab[128];
 
     const int64_t col_tiles = (cols + TILE - 1) / TILE;
@@ -115,7 +182,7 @@ quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, in
     __syncthreads();
 
     if constexpr (ROWS) {
-        // thread t takes group t % 8 of rows t / 8, + 32, + 64, + 96
+        // a thread takes one group of every (256 / groups)-th row
         const int lg = threadIdx.x & (TG - 1);
 #pragma unroll 1
         for (int row = threadIdx.x / TG; row < tile_rows; row += THREADS_T / TG) {
@@ -141,12 +208,12 @@ quantize_t_kernel(const char *__restrict__ x, int64_t ld_bytes, int64_t rows, in
     }
 
     // column groups: warp w takes row group w, a lane two neighbouring
-    // columns of each half of the tile
+    // columns of each 64 (a tile of 64 x 64 leaves half the warps idle here)
     bool nonfinite = false;
     const int rg = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (16 * rg < tile_rows) {
 #pragma unroll 1
-        for (int col = 2 * lane; col < tile_cols; col += TILE / 2) {
+        for (int col = 2 * lane; col < tile_cols; col += 64) {
             const uint8_t *p = tile + rg * 16 * PITCH + piece_at<DT>(col * ES / 16) + col * ES % 16;
             Raw<DT> a, b;
             if constexpr (DT == DT_F32) {
@@ -201,16 +268,16 @@ struct OutT {
     uint8_t *codes, *scales, *codes_t, *scales_t;
 };
 
-template <int DT, int MODE, bool ROWS>
+template <int DT, int MODE, bool ROWS, int T>
 int launch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t cols, const OutT &o,
                       const float *ts, int *err, int check_ts, cudaStream_t st, const DeviceInfo &d)
 {
-    auto kernel = quantize_t_kernel<DT, MODE, ROWS>;
-    constexpr int SMEM = smem_t_bytes<DT>();
+    auto kernel = quantize_t_kernel<DT, MODE, ROWS, T>;
+    constexpr int SMEM = Tile<DT, T>::SMEM;
     static OncePerDevice done;
     const int rc = allow_smem(kernel, SMEM, d, done);
     if (rc != IF4_OK) return rc;
-    const int64_t tiles = ((rows + TILE - 1) / TILE) * ((cols + TILE - 1) / TILE);
+    const int64_t tiles = ((rows + T - 1) / T) * ((cols + T - 1) / T);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tiles, 1, 1);
     cfg.blockDim = dim3(THREADS_T, 1, 1);
@@ -233,8 +300,41 @@ int dispatch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t col
                         const float *ts, int *err, int check_ts, cudaStream_t st,
                         const DeviceInfo &d)
 {
-    return o.codes ? launch_quantize_t<DT, MODE, true>(s, x, rows, cols, o, ts, err, check_ts, st, d)
-                   : launch_quantize_t<DT, MODE, false>(s, x, rows, cols, o, ts, err, check_ts, st, d);
+    // Small tiles while large ones make less than two blocks per SM (IF4 both ways, bf16,
+    // us with tiles of 64 / 128: 1024 x 1024 4.4 / 5.7, 2048 x 2048 7.7 / 10.0,
+    // 4096 x 2048 13.5 / 12.7, 4096 x 4096 27.0 / 22.1).
+    const int64_t large = ((rows + 127) / 128) * ((cols + 127) / 128);
+    auto run = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        return o.codes
+                   ? launch_quantize_t<DT, MODE, true, T>(s, x, rows, cols, o, ts, err, check_ts, st, d)
+                   : launch_quantize_t<DT, MODE, false, T>(s, x, rows, cols, o, ts, err, check_ts, st, d);
+    };
+    return large <= 2 * d.sm_count ? run(std::integral_constant<int, 64>{})
+                               : run(std::integral_constant<int, 128>{});
+}
+
+// ts of x, with `parts` (the column codes: 8 bytes per group) as scratch.
+int launch_scale(int x_dtype, const Shape &s, const void *x, uint32_t *parts,
+                 float *ts, cudaStream_t st, const DeviceInfo &d)
+{
+    // a block per 256 threads' first groups, up to four blocks per SM; never
+    // more than there are groups
+    const uint32_t want = (s.ngroups + 255) / 256, most = (uint32_t)d.sm_count * 4;
+    const uint32_t grid = want < most ? want : most;
+    auto amax = [&](auto k) {
+        return launch_k(k, grid, 256u, st, static_cast<const char *>(x), s.ld_bytes, s.gpr,
+                        s.ngroups, s.v8, parts);
+    };
+    int rc;
+    if (x_dtype == IF4_F32)
+        rc = amax(amax_parts_kernel<DT_F32>);
+    else if (x_dtype == IF4_BF16)
+        rc = amax(amax_parts_kernel<DT_BF16>);
+    else
+        rc = amax(amax_parts_kernel<DT_F16>);
+    if (rc != IF4_OK) return rc;
+    return launch_k(scale_parts_kernel, 1u, 256u, st, (const uint32_t *)parts, (int)grid, ts);
 }
 
 template <int MODE>
@@ -254,15 +354,18 @@ int quantize_t_entry(const void *x, int x_dtype, int64_t rows, int64_t cols, int
     DeviceInfo d;
     rc = check_device(d);
     if (rc != IF4_OK) return rc;
-    if (ts_mode == IF4_TS_COMPUTE) {
-        rc = if4_tensor_amax(x, x_dtype, rows, cols, ld_x, ts, err_flag, stream);
-        if (rc != IF4_OK) return rc;
-        rc = if4_tensor_scale(ts, ts, stream);
-        if (rc != IF4_OK) return rc;
-    }
-    if (s.ngroups == 0) return IF4_OK;
+    if (s.ngroups == 0)                // ts of an empty tensor is 1
+        return ts_mode == IF4_TS_COMPUTE
+                   ? if4_tensor_amax(x, x_dtype, rows, cols, ld_x, ts, err_flag, stream) == IF4_OK
+                         ? if4_tensor_scale(ts, ts, stream)
+                         : (int)IF4_ERR_CUDA
+                   : (int)IF4_OK;
     const int check_ts = ts_mode == IF4_TS_GIVEN ? 1 : 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (ts_mode == IF4_TS_COMPUTE) {
+        rc = launch_scale(x_dtype, s, x, reinterpret_cast<uint32_t *>(o.codes_t), ts, st, d);
+        if (rc != IF4_OK) return rc;
+    }
     switch (x_dtype) {
     case IF4_F32:
         return dispatch_quantize_t<DT_F32, MODE>(s, x, rows, cols, o, ts, err_flag, check_ts, st, d);
