@@ -807,6 +807,8 @@ rms_norm_dw_sum_kernel(const float *part, int n, int cols, float *dw)
 
 bool misaligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
+constexpr int64_t MAX_NORM_COLS = 1 << 22;
+
 int check_weight(const void *w, int w_dtype, int x_dtype)
 {
     if (w_dtype != x_dtype && w_dtype != IF4_F32) return IF4_ERR_DTYPE;
@@ -837,6 +839,7 @@ int rms_norm_quantize_entry(const void *x, int64_t ld_x, const void *res, int64_
     if (rc != IF4_OK) return rc;
     if (res && (rc = check_tensor(res, x_dtype, rows, cols, ld_res, sr)) != IF4_OK) return rc;
     if (h && (rc = check_tensor(h, x_dtype, rows, cols, ld_h, sh)) != IF4_OK) return rc;
+    if (cols > MAX_NORM_COLS) return IF4_ERR_SHAPE;
     if ((rc = check_weight(w, w_dtype, x_dtype)) != IF4_OK) return rc;
     if (!(eps > 0.0f && eps <= 3.402823466e38f)) return IF4_ERR_MODE;
     if (!ts || (s.ngroups > 0 && (!w || !codes || !scales))) return IF4_ERR_NULL;
@@ -907,7 +910,9 @@ int nvfp4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, i
 
 size_t if4_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
 {
-    if (rows < 1 || cols < 16 || cols % 16 != 0 || rows > 0x7FFFFFFF / (cols / 16)) return 0;
+    if (rows < 1 || cols < 16 || cols % 16 != 0 || cols > MAX_NORM_COLS ||
+        rows > 0x7FFFFFFF / (cols / 16))
+        return 0;
     return (size_t)std::min<int64_t>(rows, BACK_BLOCKS) * (size_t)cols * sizeof(float);
 }
 
@@ -922,6 +927,7 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
     if (rc == IF4_OK) rc = check_tensor(h, x_dtype, rows, cols, ld_h, sh);
     if (rc == IF4_OK) rc = check_tensor(dx, x_dtype, rows, cols, ld_dx, sx);
     if (rc == IF4_OK && dres) rc = check_tensor(dres, x_dtype, rows, cols, ld_dres, sr);
+    if (rc == IF4_OK && cols > MAX_NORM_COLS) rc = IF4_ERR_SHAPE;
     if (rc == IF4_OK) rc = check_weight(weight, w_dtype, x_dtype);
     if (rc != IF4_OK) return rc;
     if (cols > 0 && !dweight) return IF4_ERR_NULL;

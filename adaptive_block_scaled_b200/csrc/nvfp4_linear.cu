@@ -117,7 +117,7 @@ __device__ __forceinline__ void fence_async_smem()
 
 // The 16 scale bytes at p, of which the first nb exist (nb <= 0: none); the
 // others read as 0.  VEC: the bytes that p's and nb's alignment allows per
-// load: 16 (K % 256 == 0, aligned base), 4 (K % 64 == 0) or 2 (K % 32 == 0).
+// load: 16 (K % 256 == 0, aligned base), 4 (K % 64 == 0, aligned base) or 2.
 template <int VEC>
 __device__ __forceinline__ void load_scales16(const uint8_t *p, int nb, uint32_t (&w)[4])
 {
@@ -1274,8 +1274,8 @@ extern "C" int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, con
     if (M == 0 || N == 0) return IF4_OK;
     if (!a_codes || !a_scales || !a_ts || !b_codes || !b_scales || !b_ts || !c) return IF4_ERR_NULL;
     auto misaligned = [](const void *q, uintptr_t n) { return reinterpret_cast<uintptr_t>(q) % n != 0; };
-    if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 4) ||
-        misaligned(b_scales, 4) || misaligned(a_ts, 4) || misaligned(b_ts, 4) ||
+    if (misaligned(a_codes, 16) || misaligned(b_codes, 16) || misaligned(a_scales, 2) ||
+        misaligned(b_scales, 2) || misaligned(a_ts, 4) || misaligned(b_ts, 4) ||
         misaligned(err_flag, 4) || misaligned(c, c_dtype == IF4_F32 ? 4 : 2))
         return IF4_ERR_ALIGN;
     const size_t need = nvfp4_linear_workspace_bytes(M, N, K);
@@ -1287,7 +1287,7 @@ extern "C" int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, con
     const Problem p{a_codes, a_scales, b_codes, b_scales, a_ts, b_ts, M, N, K, workspace, c, err_flag,
                     static_cast<cudaStream_t>(stream)};
     const int vec = K % 256 == 0 && !misaligned(a_scales, 16) && !misaligned(b_scales, 16) ? 16
-                    : K % 64 == 0 ? 4 : 2;
+                    : K % 64 == 0 && !misaligned(a_scales, 4) && !misaligned(b_scales, 4) ? 4 : 2;
     auto typed = [&](auto v) {
         constexpr int V = decltype(v)::value;
         return c_dtype == IF4_F32    ? launch_linear<V, IF4_F32>(p, d)

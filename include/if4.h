@@ -370,7 +370,7 @@ int if4_linear_quantized(const uint8_t *a_codes, const uint8_t *a_scales, const 
  * c_dtype: IF4_BF16, IF4_F16 or IF4_F32; C dense.  M, N >= 0 (nothing to do at
  * 0), K >= 32, K % 32 == 0 (a row of codes is a whole number of 16-byte
  * units), M and N at most 2^22, K at most 2^20.  a_codes, b_codes 16-byte
- * aligned, a_scales, b_scales 4-byte, C aligned to its element.  workspace
+ * aligned, a_scales, b_scales 2-byte, C aligned to its element.  workspace
  * (256-byte aligned, nvfp4_linear_workspace_bytes; 0 and NULL for few rows or
  * columns) holds both operands' scales in the tensor cores' order during the
  * call; calls that may run at the same time need one each.  err_flag must not
@@ -422,9 +422,10 @@ int nvfp4_quantize_t(const void *x, int x_dtype, int64_t rows, int64_t cols, int
  * overlap an input.  rstd: float [rows].  amax: a device float that is
  * raised to max |y| (the caller zeroes it; if4_tensor_scale then gives the
  * next step's ts).  eps finite and > 0 (IF4_ERR_MODE).  x, residual, h: 16-byte
- * aligned, row strides in elements, ld*elem_size % 16 == 0.  Any number of
- * columns with cols % 16 == 0.  Inf or NaN in y sets IF4_DEV_NONFINITE (that
- * row's codes are unspecified).  Other rules as if4_quantize.
+ * aligned, row strides in elements, ld*elem_size % 16 == 0.  cols % 16 == 0,
+ * at most 2^22.  Inf or NaN in y sets IF4_DEV_NONFINITE (that
+ * row's codes and rstd, and amax, are unspecified).  Other rules as
+ * if4_quantize.
  */
 int if4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, int64_t ld_res,
                           const void *weight, int w_dtype, int x_dtype, int64_t rows, int64_t cols,

@@ -169,6 +169,19 @@ def test_alignment_and_no_writes_outside(M, N, K, dtype):
     assert float(flat[0]) == 7.0 and torch.all(flat[1 + M * N:] == 7.0)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 100, 96), (2, 100, 512), (9, 100, 96), (9, 100, 512),
+                                   (150, 200, 96), (150, 200, 512), (150, 200, 1056)])
+def test_rows_of_larger_operands(M, N, K):
+    """Views that begin at an odd row: scales on a 2-byte boundary."""
+    g = torch.Generator().manual_seed(K)
+    a, b = cuda(operand(M + 3, K, g)), cuda(operand(N + 1, K, g))
+    one = torch.full((1,), 2.0 ** -8, device="cuda")
+    a, b = tuple(t[3:] for t in a), tuple(t[1:] for t in b)
+    c, err = run(a, b, one, one, torch.float32)
+    assert int(err) == 0
+    check(c, a, b, one, one)
+
+
 def test_empty():
     bb = B()
     z = torch.zeros(1, device="cuda")

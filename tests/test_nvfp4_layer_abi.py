@@ -44,7 +44,7 @@ def test_linear_refusals(lib):
                dict(M=(1 << 22) + 1), dict(N=(1 << 22) + 1), dict(K=(1 << 20) + 32)):
         assert linear(lib, **kw) == 2, kw
     assert linear(lib, dt=3) == 3 and linear(lib, dt=-1) == 3
-    for kw in (dict(ac=A + 8), dict(bc=A + 8), dict(asc=A + 2), dict(bs=A + 2), dict(at=A + 2),
+    for kw in (dict(ac=A + 8), dict(bc=A + 8), dict(asc=A + 1), dict(bs=A + 1), dict(at=A + 2),
                dict(bt=A + 1), dict(c=A + 1), dict(c=A + 2, dt=0), dict(err=A + 2),
                dict(M=256, N=256, ws=A + 128)):
         assert linear(lib, **kw) == 4, kw
@@ -96,7 +96,9 @@ def test_rms_norm_quantize_refusals(lib, mode):
 
     for k in ("x", "w", "co", "s", "ts"):
         assert call(**{k: None}) == 1, k
-    for kw in (dict(c=40), dict(r=-1), dict(ldx=32), dict(ldr=32), dict(ldh=32)):
+    wide = (1 << 22) + 16
+    for kw in (dict(c=40), dict(r=-1), dict(ldx=32), dict(ldr=32), dict(ldh=32),
+               dict(c=wide, ldx=wide, ldr=wide, ldh=wide)):
         assert call(**kw) == 2, kw
     for kw in (dict(dt=4), dict(wdt=2), dict(wdt=7), dict(dt=0, wdt=1)):
         assert call(**kw) == 3, kw
@@ -127,7 +129,7 @@ def test_rms_norm_backward_refusals(lib):
     assert need == 4 * 64 * 4
     assert call(ws=None) == 6 and call(n=need - 1) == 6
     assert lib.if4_rms_norm_backward_workspace_bytes(1 << 20, 64) == 296 * 64 * 4
-    for bad in ((0, 64), (4, 0), (4, 40), (1 << 31, 64)):
+    for bad in ((0, 64), (4, 0), (4, 40), (1 << 31, 64), (1, (1 << 22) + 16)):
         assert lib.if4_rms_norm_backward_workspace_bytes(*bad) == 0
 
 
