@@ -88,7 +88,7 @@ struct OutQ {
 __device__ __forceinline__ void out_inv_table(float *inv_tab, const float *c_ts, int *err)
 {
     if (threadIdx.x < 128) {
-        const float ts = *c_ts;
+        const float ts = ld_after_wait(c_ts);
         const float eff = __fmul_rn(f32_from_e4m3(threadIdx.x), ts);
         inv_tab[threadIdx.x] = threadIdx.x == 0 ? 0.0f : __frcp_rn(eff);
         if (threadIdx.x == 0 && blockIdx.x == 0 && !(ts >= 0x1p-117f && ts <= 0x1p117f) && err)
@@ -295,10 +295,10 @@ gemm_f16_tcgen05(const __grid_constant__ CUtensorMap tmap_a,
         // -------------------------------------------------------- epilogue
         const int quarter = warp & 3;                 // TMEM lanes this warp may read
         const int row_in_tile = quarter * 32 + lane;
-        const float scale = __fmul_rn(*a_ts, *b_ts);
+        const float scale = __fmul_rn(ld_after_wait(a_ts), ld_after_wait(b_ts));
         OutQ oq{c_codes, c_scales, 1.0f, 1.0f, inv_tab};
         if constexpr (QOUT) {
-            oq.ts = *c_ts;
+            oq.ts = ld_after_wait(c_ts);
             oq.rts = __frcp_rn(oq.ts);
         }
         bool nonfinite = false;
@@ -502,10 +502,10 @@ gemm_f16_tcgen05_2sm(const __grid_constant__ CUtensorMap tmap_a,
         // -------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const int row_in_cta = quarter * 32 + lane;
-        const float scale = __fmul_rn(*a_ts, *b_ts);
+        const float scale = __fmul_rn(ld_after_wait(a_ts), ld_after_wait(b_ts));
         OutQ oq{c_codes, c_scales, 1.0f, 1.0f, inv_tab};
         if constexpr (QOUT) {
-            oq.ts = *c_ts;
+            oq.ts = ld_after_wait(c_ts);
             oq.rts = __frcp_rn(oq.ts);
         }
         bool nonfinite = false;
@@ -880,7 +880,7 @@ gemm_if4_fused_2sm(const uint8_t *__restrict__ a_codes, const uint8_t *__restric
         // -------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const int row_in_cta = quarter * 32 + lane;
-        const float scale = __fmul_rn(*a_ts, *b_ts);
+        const float scale = __fmul_rn(ld_after_wait(a_ts), ld_after_wait(b_ts));
         const OutQ oq{nullptr, nullptr, 1.0f, 1.0f, nullptr};
         const uint32_t acc_empty_leader0 = map_to(smem_u32(&acc_empty[0]), 0);
         const uint32_t acc_empty_leader1 = map_to(smem_u32(&acc_empty[1]), 0);

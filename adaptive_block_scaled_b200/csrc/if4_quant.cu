@@ -557,7 +557,7 @@ quantize_kernel(const char *__restrict__ x, int64_t ld_bytes, uint32_t gpr,
 {
     pdl_enter();
     constexpr int GB = 16 * elem_bytes<DT>();
-    const float ts = *ts_ptr;
+    const float ts = ld_after_wait(ts_ptr);
     if (check_ts && blockIdx.x == 0 && threadIdx.x == 0 && !ts_valid(ts) && err)
         atomicOr(err, IF4_DEV_BAD_SCALE);
     __shared__ float inv_tab[128];
@@ -889,7 +889,7 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
     constexpr int OB = ODT == DT_F32 ? 4 : 2;
     __shared__ __align__(128) float lut[32];
     if (threadIdx.x < 32) lut[threadIdx.x] = code_value(threadIdx.x);
-    const float ts = UNIT_TS ? 1.0f : *ts_ptr;
+    const float ts = UNIT_TS ? 1.0f : ld_after_wait(ts_ptr);
     const uint32_t lut_addr = (uint32_t)__cvta_generic_to_shared(lut);
     __syncthreads();
     const uint32_t stride = gridDim.x * blockDim.x;

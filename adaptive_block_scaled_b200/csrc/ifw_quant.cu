@@ -542,7 +542,7 @@ ifw_quantize_kernel(const char *__restrict__ x, int64_t ld_bytes, uint32_t gpr, 
     constexpr int CB = Width<BITS>::code_bytes;
     __shared__ float int_tab[1 << BITS];
     fill_int_table<BITS>(int_tab);
-    const float ts = *ts_ptr;
+    const float ts = ld_after_wait(ts_ptr);
     if (check_ts && blockIdx.x == 0 && threadIdx.x == 0 && !ts_ok(ts) && err)
         atomicOr(err, IF4_DEV_BAD_SCALE);
     const float c_int = BITS == 6 ? __fdiv_rn(62.0f, 15.0f) : 0.75f;
@@ -667,7 +667,7 @@ ifw_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restri
     __shared__ float fp_tab[1 << BITS];
     fill_int_table<BITS>(int_tab);
     for (int c = threadIdx.x; c < (1 << BITS); c += blockDim.x) fp_tab[c] = fp_value<BITS>(c);
-    const float ts = *ts_ptr;
+    const float ts = ld_after_wait(ts_ptr);
     __syncthreads();
     const bool contig = ld_bytes == (int64_t)gpr * (16 * OB);
     // a dense, 32-byte aligned output: every group's outputs start on a
