@@ -781,18 +781,25 @@ rms_norm_dw_kernel(const __grid_constant__ BackArgs a)
     a.part[(int64_t)blockIdx.x * a.gpr * 16 + col] = s;
 }
 
-// dw: n partial rows.  A block takes 32 columns; warp v adds rows v, v + 32,
-// ..., then one warp adds the 32 sums in order.
+// dw: n <= BACK_BLOCKS partial rows.  A block takes 32 columns; warp v adds rows
+// v, v + 32, ..., all loaded before they are added, then one warp adds the 32
+// sums in order.
 __global__ void __launch_bounds__(1024)
 rms_norm_dw_sum_kernel(const float *part, int n, int cols, float *dw)
 {
     pdl_enter();
     __shared__ float sums[32][33];
+    constexpr int PER = (BACK_BLOCKS + 31) / 32;
     const int lane = threadIdx.x & 31, v = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    if (col < cols)
-        for (int i = v; i < n; i += 32) s += ld_after_wait(part + (int64_t)i * cols + col);
+    float x[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        x[i] = col < cols && v + 32 * i < n ? ld_after_wait(part + (int64_t)(v + 32 * i) * cols + col)
+                                            : 0.0f;
+    float s = x[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) s = __fadd_rn(s, x[i]);
     sums[v][lane] = s;
     __syncthreads();
     if (v == 0 && col < cols) {
