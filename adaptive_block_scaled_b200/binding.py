@@ -439,20 +439,28 @@ def nvfp4_linear_workspace_bytes(M, N, K):
     return lib.nvfp4_linear_workspace_bytes(M, N, K)
 
 
+def _operand(codes, scales, ts, name):
+    """Rows and code bytes per row of an NVFP4 operand."""
+    if codes.dim() != 2:
+        raise ValueError(f"{name}_codes must be 2-D")
+    rows, kb = codes.shape
+    if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8
+            or scales.shape != (rows, kb // 8) or not codes.is_contiguous()
+            or not scales.is_contiguous() or ts.dtype is not torch.float32 or ts.numel() < 1):
+        _dense(codes, f"{name}_codes", torch.uint8, (rows, kb))
+        _dense(scales, f"{name}_scales", torch.uint8, (rows, kb // 8))
+        _word(ts, f"{name}_ts", torch.float32)
+    return rows, kb
+
+
 def _nvfp4_linear(a, b, ws, c, err_flag, stream):
     """Checks the operands (not c and ws) and calls nvfp4_linear."""
     (a_codes, a_scales, a_ts), (b_codes, b_scales, b_ts) = a, b
     dev = _device("nvfp4_linear", a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, c, err_flag)
-    if a_codes.dim() != 2 or b_codes.dim() != 2:
-        raise ValueError("a_codes and b_codes must be 2-D")
-    (M, kb), N = a_codes.shape, b_codes.shape[0]
-    u8, f32 = torch.uint8, torch.float32
-    _dense(a_codes, "a_codes", u8, (M, kb))
-    _dense(a_scales, "a_scales", u8, (M, kb // 8))
-    _dense(b_codes, "b_codes", u8, (N, kb))
-    _dense(b_scales, "b_scales", u8, (N, kb // 8))
-    _word(a_ts, "a_ts", f32)
-    _word(b_ts, "b_ts", f32)
+    M, kb = _operand(a_codes, a_scales, a_ts, "a")
+    N, kb_b = _operand(b_codes, b_scales, b_ts, "b")
+    if kb_b != kb:
+        raise ValueError(f"a_codes has rows of {kb} bytes, b_codes of {kb_b}")
     _word(err_flag, "err_flag", torch.int32)
     wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     _call("nvfp4_linear", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), a_ts.data_ptr(),

@@ -789,6 +789,60 @@ __device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float sca
     }
 }
 
+// Two-byte C whose rows begin anywhere: COLS columns of the warp's 32 rows
+// (lane: row) into its shared memory as pairs, from column `off` of 64 ...
+template <int ODT, int COLS>
+__device__ __forceinline__ void stage_pairs(const uint32_t *r, float scale, int off, uint32_t *stage)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < COLS / 2; ++i) {
+        const float lo = __fmul_rn(__uint_as_float(r[2 * i]), scale);
+        const float hi = __fmul_rn(__uint_as_float(r[2 * i + 1]), scale);
+        stage[lane * 33 + off / 2 + i] =
+            ODT == IF4_BF16 ? bf16x2_from_f32(lo, hi) : f16x2_from_f32(lo, hi);
+    }
+}
+
+// ... and out row by row, a four-byte store per lane: pairs as they lie where
+// the row's first element is on a four-byte boundary, else pairs shifted by
+// one element and the two ends by themselves.  Four warps write the whole tile,
+// so what counts is that eight rows' reads are under way at once: 8192 x 4097 x
+// 4096 88 us; row after row 126, an element per lane and store 105.
+__device__ __forceinline__ void flush_pairs(void *c, int row0, int M, int N, int col0, int cols,
+                                            uint32_t *stage)
+{
+    const int lane = threadIdx.x & 31;
+    const int rows = min(32, M - row0);
+    cols = min(cols, N - col0);
+    __syncwarp();
+    uint16_t *p = static_cast<uint16_t *>(c) + (int64_t)row0 * N + col0;
+    const uint32_t *in = stage + lane;
+    const int next = lane < 31 ? 1 : 0;
+#pragma unroll 1
+    for (int q = 0; q < rows; q += 8) {
+        uint32_t w0[8], w1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w0[i] = in[(q + i) * 33];
+            w1[i] = in[(q + i) * 33 + next];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint16_t *d = p + (int64_t)(q + i) * N;
+            const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(d) >> 1) & 1u;
+            const int first = 2 * lane + (int)odd;
+            const uint32_t v = __funnelshift_r(w0[i], w1[i], 16 * odd);
+            const bool in_row = q + i < rows;
+            if (in_row && first + 1 < cols) *reinterpret_cast<uint32_t *>(d + first) = v;
+            // the last element alone, and (lane 0) the first
+            if (in_row && first + 1 == cols) d[first] = (uint16_t)v;
+            if (in_row && odd && lane == 0 && cols > 0) d[0] = (uint16_t)w0[i];
+        }
+    }
+    __syncwarp();
+}
+
 // The same for two-byte C whose rows are multiples of 16 bytes, 32 whole
 // columns: through shared memory (64-byte rows, swizzled as the tensor map
 // says) and a TMA store, which writes whole lines and clips at C's edges
@@ -1003,6 +1057,10 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
                         store_box<ODT>(&tmap_c, r, scale, row0, n0 + col, boxes + box * OUT_BOX);
                         box ^= 1;          // only a box that was stored takes a buffer
                     }
+                } else if (ODT != IF4_F32) {
+                    stage_pairs<ODT, 32>(r, scale, col & 32, stage);
+                    if ((col & 32) || col + 32 == BN)
+                        flush_pairs(c, row0, M, N, n0 + (col & ~32), (col & 32) + 32, stage);
                 } else {
                     store_cols<ODT, 32>(c, r, scale, row0, M, N, n0 + col, width, stage);
                 }
@@ -1017,13 +1075,19 @@ nvfp4_linear_pair(const __grid_constant__ CUtensorMap tmap_a,
             if constexpr (BN % 32 != 0) {
                 uint32_t q[16];
                 tmem_ld16(base + BN / 32 * 32, q);
-                const int col = n0 + BN / 32 * 32;
-                // element stores at C's edge go through the boxes' memory
-                if (box_stores && col + 16 > N) {
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    __syncwarp();
+                constexpr int LAST = BN / 32 * 32;
+                if (ODT != IF4_F32 && !box_stores) {
+                    // with the 32 columns that wait, if any do
+                    stage_pairs<ODT, 16>(q, scale, LAST & 32, stage);
+                    flush_pairs(c, row0, M, N, n0 + (LAST & ~32), (LAST & 32) + 16, stage);
+                } else {
+                    // element stores at C's edge go through the boxes' memory
+                    if (box_stores && n0 + LAST + 16 > N) {
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                    }
+                    store_cols<ODT, 16>(c, q, scale, row0, M, N, n0 + LAST, width, stage);
                 }
-                store_cols<ODT, 16>(c, q, scale, row0, M, N, col, width, stage);
             }
             tc_fence_before();
             __syncwarp();
