@@ -49,6 +49,15 @@ int check_device(DeviceInfo &d)
     return IF4_OK;
 }
 
+// Status of a launch.  A failed one leaves nothing in the runtime's last error,
+// which the next call would take for its own.
+inline int launched(cudaError_t e)
+{
+    if (e == cudaSuccess) return IF4_OK;
+    (void)cudaGetLastError();
+    return IF4_ERR_CUDA;
+}
+
 // Raises a kernel's dynamic shared-memory limit, once per device (a race only
 // repeats the call; nothing here throws).
 typedef std::atomic<bool> OncePerDevice[MAX_DEVICES];
@@ -57,9 +66,9 @@ template <typename Kernel>
 int allow_smem(Kernel kernel, int bytes, const DeviceInfo &d, OncePerDevice &done)
 {
     if (!done[d.id].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-            cudaSuccess)
-            return IF4_ERR_CUDA;
+        const int rc = launched(
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+        if (rc != IF4_OK) return rc;
         done[d.id].store(true, std::memory_order_release);
     }
     return IF4_OK;
@@ -121,8 +130,7 @@ int launch_k(void (*k)(KArgs...), unsigned grid, unsigned block, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k, args...) != cudaSuccess) return IF4_ERR_CUDA;
-    return launch_status();
+    return launched(cudaLaunchKernelEx(&cfg, k, args...));
 }
 
 }  // namespace

@@ -948,9 +948,7 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
     if (rc != IF4_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (sy.ngroups == 0) {                // no rows: dweight is an empty sum
-        if (cols > 0 && cudaMemsetAsync(dweight, 0, (size_t)cols * 4, st) != cudaSuccess)
-            return IF4_ERR_CUDA;
-        return IF4_OK;
+        return cols > 0 ? launched(cudaMemsetAsync(dweight, 0, (size_t)cols * 4, st)) : IF4_OK;
     }
     const BackArgs a{static_cast<const char *>(dy), static_cast<const char *>(h),
                      static_cast<const char *>(weight), static_cast<const char *>(dres),
@@ -991,9 +989,7 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
                 attr[0].val.programmaticStreamSerializationAllowed = 1;
                 cfg.attrs = attr;
                 cfg.numAttrs = 1;
-                if (cudaLaunchKernelEx(&cfg, kernel, a, T) != cudaSuccess)
-                    return (int)IF4_ERR_CUDA;
-                return launch_status();
+                return launched(cudaLaunchKernelEx(&cfg, kernel, a, T));
             };
             int r;
             if constexpr (DT != DT_F32)
@@ -1009,9 +1005,9 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
         cfg.gridDim = dim3((unsigned)parts, (unsigned)((cols + 255) / 256), 1);
         cfg.blockDim = dim3(256, 1, 1);
         cfg.stream = st;
-        if (cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel<DT>, a) != cudaSuccess)
-            return (int)IF4_ERR_CUDA;
-        const int r = sum_dw(parts);
+        int r = launched(cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel<DT>, a));
+        if (r != IF4_OK) return r;
+        r = sum_dw(parts);
         if (r != IF4_OK) return r;
         return launch_k(rms_norm_dx_kernel<DT, WT>,
                         (unsigned)std::min<int64_t>(rows, (int64_t)d.sm_count * 8),

@@ -11,8 +11,8 @@
 //
 // A block takes a tile of 128 x 128 (64 x 64 for small tensors) into shared
 // memory with asynchronous 16-byte copies, which hold no registers while they
-// are under way.  Row form: a thread reads whole row groups (16 values, 32 or 64 bytes) and encodes them.
-// Column form: a thread reads 16 rows of two neighbouring columns (one
+// are under way.  Row form: a thread reads whole row groups (16 values, 32 or
+// 64 bytes) and encodes them.  Column form: a thread reads 16 rows of two neighbouring columns (one
 // conflict-free word per row), which are two whole column groups in registers,
 // and encodes them with the same group encoder.  The column codes are put back
 // in order through shared memory, so that a tile's code bytes of a column leave
@@ -306,11 +306,9 @@ int launch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t cols,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<const char *>(x), s.ld_bytes, rows, cols,
-                           o.codes, o.scales, o.codes_t, o.scales_t, ts, err, check_ts) !=
-        cudaSuccess)
-        return IF4_ERR_CUDA;
-    return launch_status();
+    return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<const char *>(x), s.ld_bytes, rows,
+                                       cols, o.codes, o.scales, o.codes_t, o.scales_t, ts, err,
+                                       check_ts));
 }
 
 template <int DT, int MODE>
@@ -325,11 +323,11 @@ int dispatch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t col
     auto run = [&](auto t) {
         constexpr int T = decltype(t)::value;
         return o.codes
-                   ? launch_quantize_t<DT, MODE, true, T>(s, x, rows, cols, o, ts, err, check_ts, st, d)
-                   : launch_quantize_t<DT, MODE, false, T>(s, x, rows, cols, o, ts, err, check_ts, st, d);
+            ? launch_quantize_t<DT, MODE, true, T>(s, x, rows, cols, o, ts, err, check_ts, st, d)
+            : launch_quantize_t<DT, MODE, false, T>(s, x, rows, cols, o, ts, err, check_ts, st, d);
     };
     return large <= 2 * d.sm_count ? run(std::integral_constant<int, 64>{})
-                               : run(std::integral_constant<int, 128>{});
+                                   : run(std::integral_constant<int, 128>{});
 }
 
 // ts of x, with `parts` (the column codes: 8 bytes per group) as scratch.

@@ -2,7 +2,8 @@
 // 4-bit codes, on the block-scaled tensor cores.
 //
 // With q the E2M1 values and s the E4M3 block scales of groups of 16 along K,
-//   C[m, n] = out( fl(a_ts * b_ts) * sum_g a_s[m, g] b_s[n, g] sum_{i<16} a_q[m, 16 g + i] b_q[n, 16 g + i] ).
+//   C[m, n] = out( fl(a_ts * b_ts) *
+//                  sum_g a_s[m, g] b_s[n, g] sum_{i<16} a_q[m, 16 g + i] b_q[n, 16 g + i] ).
 // tcgen05.mma kind::mxf4nvf4 with a scale per 16 elements evaluates the double
 // sum from the codes as they are stored (two per byte, the first in the low
 // nibble, K contiguous) and the scale bytes as UE4M3, accumulating in binary32
@@ -15,9 +16,11 @@
 // quarters) fills that from 512 contiguous bytes of shared memory, row m's 4
 // bytes at (m % 32) * 16 + (m / 32) * 4.  The scales of a row lie K / 16
 // bytes apart from the next row's, so no tiled copy makes this order from
-// them: scale warps load 16 bytes per row and 256 of K into registers and
-// store them as four words, one per K step.  They work in units of 512 of K,
-// so that the two lanes of a row use a whole 32-byte sector.
+// them: they go through registers, 16 bytes per row and 256 of K, and leave as
+// four words, one per K step.  Work comes in units of 512 of K, so that the
+// two lanes of a row use a whole 32-byte sector.  With few rows the kernel's
+// own warps do that beside the MMAs; with many rows a kernel in front of it does,
+// once for all the tiles that share a row.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -182,8 +185,8 @@ __device__ __forceinline__ void store_c(void *c, int64_t i, float v)
 //
 // Nothing here waits for anything but the loads: no tensor memory, barrier
 // or cluster stands between the launch and them.  A token of 4096 x 4096 takes
-// 3.0 us (5.7 with the kernel below; the weight's bytes are 1.5), two tokens
-// 4.2 (5.8).  The conversions bound it: four tokens take 7.3 us (5.8), and a
+// 3.0 to 3.8 us from run to run (5.7 with the kernel below; the weight's bytes
+// are 1.5), two tokens 4.2 (5.8).  The conversions bound it: four tokens take 7.3 us (5.8), and a
 // token of 16384 x 4096 11.1 (10.0).  Two columns per warp and eight warps per
 // block, all loads of a chunk up front: four columns took 4.5 us, one 3.7, four
 // warps 3.4.
@@ -732,7 +735,8 @@ pack_scales(ScalePack a, ScalePack b, int K, int *err)
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
                                                  int z, uint32_t bar_cluster)
 {
-    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global"
+                 ".mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z),
                     "r"(bar_cluster)
@@ -743,7 +747,9 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 // to C's type.  width: bytes that C's base and row length allow per store, 32
 // or 16; 0: elements only.  Then a lane's stores would touch a sector each for
 // two or four bytes, so the block goes through the warp's shared memory (rows
-// of 33 words) and leaves row by row, lanes along the columns.
+// of 33 words) and leaves row by row, lanes along the columns.  (Two-byte C: only
+// the last 16 columns of a 240-wide tile come here, its other blocks leave as
+// boxes or pairs, below.)
 template <int ODT, int COLS>
 __device__ __forceinline__ void store_cols(void *c, const uint32_t *r, float scale, int row0, int M,
                                            int N, int col0, int width, uint32_t *stage)
@@ -1176,10 +1182,8 @@ int launch_split(const Problem &p, const DeviceInfo &d, int ranks)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, mw, mx, p.b_scales, p.a_scales, p.b_ts, p.a_ts, p.c,
-                           (int)p.M, (int)p.N, (int)p.K, p.err) != cudaSuccess)
-        return IF4_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, mw, mx, p.b_scales, p.a_scales, p.b_ts, p.a_ts,
+                                       p.c, (int)p.M, (int)p.N, (int)p.K, p.err));
 }
 
 // Two-byte C [M, N] -> tensor map with a box of 32 columns x 32 rows.
@@ -1252,8 +1256,8 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
     const int64_t blocks = (warps + 7) / 8, most = (int64_t)d.sm_count * 8;
     cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
-    if (cudaLaunchKernelEx(&cfg, pack_scales<VEC>, sa, sb, (int)p.K, p.err) != cudaSuccess)
-        return IF4_ERR_CUDA;
+    const int packed = launched(cudaLaunchKernelEx(&cfg, pack_scales<VEC>, sa, sb, (int)p.K, p.err));
+    if (packed != IF4_OK) return packed;
 
     cfg.gridDim = dim3((unsigned)(2 * (d.sm_count / 2)), 1, 1);
     cfg.blockDim = dim3(duo::THREADS, 1, 1);
@@ -1278,10 +1282,8 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
     const int64_t tiles = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + BN - 1) / BN);
     const int64_t pairs = tiles < pairs_max ? tiles : pairs_max;
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mc, boxes ? 1 : 0, p.a_ts, p.b_ts, p.c, (int)p.M, (int)p.N,
-                           (int)p.K, p.err) != cudaSuccess)
-        return IF4_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? IF4_OK : IF4_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mc, boxes ? 1 : 0, p.a_ts,
+                                       p.b_ts, p.c, (int)p.M, (int)p.N, (int)p.K, p.err));
 }
 
 template <int VEC, int ODT>
