@@ -612,9 +612,10 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
                 const Unit<WT> w = U == 1 ? w1 : weight(t + k * T);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const f2_t dh = f2_mul(pair_of(d, j), pair_of(h, j));
-                    acc = f2_fma(dh, pair_of(w, j), acc);
-                    dw[k][j] = f2_fma(dh, RS, dw[k][j]);
+                    // (n first: dy * h may leave binary32's range where dy * n does not)
+                    const f2_t n = f2_mul(pair_of(h, j), RS), dy = pair_of(d, j);
+                    dw[k][j] = f2_fma(dy, n, dw[k][j]);
+                    acc = f2_fma(f2_mul(dy, pair_of(w, j)), n, acc);
                 }
             }
         if constexpr (U == 1) fetch(row + R::S * step, stage);
@@ -634,7 +635,7 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         }
         // mean(g * n) * rstd, n = h * rstd
-        const float c = s * rstd * rstd * a.inv_cols;
+        const float c = s * rstd * a.inv_cols;
         const f2_t NC = f2_pack(-c, -c);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -709,6 +710,7 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
     constexpr int GB = 16 * elem_bytes<DT>();
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float rstd = a.rstd[row];
+        const f2_t RS = f2_pack(rstd, rstd);
         float s = 0.0f;
         for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
             Raw<DT> hr, dr;
@@ -722,15 +724,15 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
             to_pairs<WT>(wr, w);
             f2_t acc = f2_pack(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc = f2_fma(f2_mul(d[j], w[j]), h[j], acc);
+            for (int j = 0; j < 8; ++j) acc = f2_fma(f2_mul(d[j], w[j]), f2_mul(h[j], RS), acc);
             float lo, hi;
             f2_unpack(acc, lo, hi);
             s += lo + hi;
         }
         s = block_sum(s, sums);
         // mean(g * n) * rstd, n = h * rstd
-        const float k = s * rstd * rstd * a.inv_cols;
-        const f2_t RS = f2_pack(rstd, rstd), NK = f2_pack(-k, -k);
+        const float k = s * rstd * a.inv_cols;
+        const f2_t NK = f2_pack(-k, -k);
         for (int g = threadIdx.x; g < a.gpr; g += NORM_THREADS) {
             Raw<DT> hr, dr, er;
             Raw<WT> wr;

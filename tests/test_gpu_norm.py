@@ -258,6 +258,18 @@ def test_backward_many_rows():
     check_backward(r, x, w, r)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [400, 16384, 33024])
+def test_backward_products_past_float32(cols, dtype):
+    """dy * h leaves binary32's range, dy * n and the gradients do not."""
+    x, r, w = data(19, cols, dtype, 12)
+    h, dy = x.float(), r.float()
+    h[::3] *= 1e30
+    dy[::2] *= 1e12
+    h[1] = 0.0
+    check_backward(dy.to(dtype), h.to(dtype), w, None)
+
+
 @pytest.mark.parametrize("cols", [400, 4096, 33024])
 @pytest.mark.parametrize("which", ["dy", "dres"])
 def test_backward_in_place(which, cols):
