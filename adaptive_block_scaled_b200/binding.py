@@ -481,14 +481,18 @@ def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
 
 def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
     """a, b: (codes, scales, ts) of NVFP4 operands [M, K] and [N, K].  Returns
-    A B^T [M, N] of dtype."""
+    A B^T [M, N] of dtype.  With a stream, the result and the workspace are
+    allocated on it, as under torch.cuda.stream (so in the helpers below)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_nvfp4(a, b, dtype, err_flag)
     (M, kb), N, dev = a[0].shape, b[0].shape[0], a[0].device
     c = _new(M, N, dtype, dev)
     if err_flag is None:
         err_flag = torch.zeros(1, dtype=torch.int32, device=dev)
     need = lib.nvfp4_linear_workspace_bytes(M, N, 2 * kb)
     ws = _new1(need, torch.uint8, dev) if need else None
-    _nvfp4_linear(a, b, ws, c, err_flag, stream)
+    _nvfp4_linear(a, b, ws, c, err_flag, None)
     return c
 
 
@@ -544,6 +548,9 @@ def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=No
     Returns (codes_t, scales_t, ts) of x^T or, with_rows, (codes, scales,
     codes_t, scales_t, ts) of x and of x^T under one tensor scale.  ts=None
     computes it; a float32 tensor is used as given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_t(x, mode, ts, with_rows, err_flag)
     entry = _entry(mode, "quantize_t")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
@@ -556,7 +563,7 @@ def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=No
         ts, ts_mode = _new1(1, torch.float32, dev), TS_COMPUTE
     else:
         ts_mode = TS_GIVEN
-    _quantize_t(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, stream)
+    _quantize_t(entry, x, codes, scales, codes_t, scales_t, ts, ts_mode, err_flag, None)
     if with_rows:
         return codes, scales, codes_t, scales_t, ts
     return codes_t, scales_t, ts
@@ -617,6 +624,9 @@ def rms_norm_quantize(x, weight, ts, residual=None, eps=1e-6, mode="if4", amax=N
     the float32 tensor ts.  Returns (codes, scales, h, rstd): h = x + residual
     (x itself without a residual) and rstd [rows] are what rms_norm_backward
     takes.  amax: a float32 tensor raised to max |y|, for the next ts."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_quantize(x, weight, ts, residual, eps, mode, amax, err_flag)
     entry = _entry(mode, "rms_norm_quantize")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
@@ -624,7 +634,7 @@ def rms_norm_quantize(x, weight, ts, residual=None, eps=1e-6, mode="if4", amax=N
     codes, scales = _new(rows, cols // 2, torch.uint8, dev), _new(rows, cols // 16, torch.uint8, dev)
     rstd = _new1(rows, torch.float32, dev)
     h = None if residual is None else _new(rows, cols, x.dtype, dev)
-    _rms_norm(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag, stream)
+    _rms_norm(entry, x, residual, weight, eps, h, rstd, codes, scales, ts, amax, err_flag, None)
     return codes, scales, x if h is None else h, rstd
 
 
@@ -654,11 +664,14 @@ def rms_norm_backward(dy, h, weight, rstd, dres=None, stream=None):
     """Gradient of rms_norm_quantize (straight through the quantizer) from dy,
     the gradient of the norm's output, and dres, that of h past the norm.
     Returns (dx, dweight): dx for x and the residual alike, dweight float32."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_backward(dy, h, weight, rstd, dres)
     (rows, cols), dev = h.shape, h.device
     dx, dweight = _new(rows, cols, h.dtype, dev), _new1(cols, torch.float32, dev)
     need = lib.if4_rms_norm_backward_workspace_bytes(rows, cols)
     ws = _new1(need, torch.uint8, dev) if need else None
-    if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, ws, stream)
+    if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, ws)
     return dx, dweight
 
 

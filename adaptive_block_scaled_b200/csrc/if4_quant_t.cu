@@ -12,11 +12,11 @@
 // A block takes a tile of 128 x 128 (64 x 64 for small tensors) into shared
 // memory with asynchronous 16-byte copies, which hold no registers while they
 // are under way.  Row form: a thread reads whole row groups (16 values, 32 or
-// 64 bytes) and encodes them.  Column form: a thread reads 16 rows of two neighbouring columns (one
-// conflict-free word per row), which are two whole column groups in registers,
-// and encodes them with the same group encoder.  The column codes are put back
-// in order through shared memory, so that a tile's code bytes of a column leave
-// as one run.
+// 64 bytes) and encodes them.  Column form: a thread reads 16 rows of two
+// neighbouring columns (one conflict-free word per row), which are two whole
+// column groups in registers, and encodes them with the same group encoder.
+// The column codes are put back in order through shared memory, so that a
+// tile's code bytes of a column leave as one run.
 //
 // With both forms and IF4 the encoder's instructions bound it (two encodes of
 // about 200 instructions per 16 values, 270 in all): 8192 x 8192 bf16 with the
@@ -316,8 +316,8 @@ int dispatch_quantize_t(const Shape &s, const void *x, int64_t rows, int64_t col
                         const float *ts, int *err, int check_ts, cudaStream_t st,
                         const DeviceInfo &d)
 {
-    // Small tiles while large ones make less than two blocks per SM (IF4 both ways, bf16,
-    // us with tiles of 64 / 128: 1024 x 1024 4.4 / 5.7, 2048 x 2048 7.7 / 10.0,
+    // Small tiles while large ones make less than two blocks per SM (IF4 both
+    // ways, bf16, us with tiles of 64 / 128: 1024 x 1024 4.4 / 5.7, 2048 x 2048 7.7 / 10.0,
     // 4096 x 2048 13.5 / 12.7, 4096 x 4096 27.0 / 22.1).
     const int64_t large = ((rows + 127) / 128) * ((cols + 127) / 128);
     auto run = [&](auto t) {

@@ -139,6 +139,38 @@ def test_two_streams_at_once():
         assert all(torch.equal(p, q) for r in o for p, q in zip(r, wnt))
 
 
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_helpers_on_a_given_stream_share_no_memory_with_the_current_one(M):
+    """Work on a side stream that is still waiting, while the current stream
+    takes and fills every block that a helper could have returned to it."""
+    bb = B()
+    N, K = 512, 1024
+    x, r, wn, w, dy = layer_inputs(304, N, K, M)
+    x, r = x[:M], r[:M]
+    ts = torch.tensor([0.005], device="cuda")
+    b = bb.quantize(w, "nvfp4")
+
+    def step(st):
+        codes, scales, h, rstd = bb.rms_norm_quantize(x, wn, ts, residual=r, mode="nvfp4", stream=st)
+        c = bb.linear_nvfp4((codes, scales, ts), b, stream=st)
+        dx, dwn = bb.rms_norm_backward(h, h, wn, rstd, stream=st)
+        return (codes, scales, h, rstd, c, dx, dwn, *bb.quantize_t(dy, "nvfp4", stream=st))
+
+    want = step(None)
+    torch.cuda.synchronize()
+    sizes = [bb.lib.nvfp4_linear_workspace_bytes(M, N, K),
+             bb.lib.if4_rms_norm_backward_workspace_bytes(M, K), 4, 4 * M]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = step(side)
+    fill = [torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+            for n in sizes for _ in range(4) if n]
+    torch.cuda.synchronize()
+    assert all(bool(torch.all(f == 0xA5)) for f in fill)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second device")
 def test_tensors_on_another_device_than_the_current_one():
     bb = B()
