@@ -342,13 +342,13 @@ constexpr int SF_UNITS = 3;
 constexpr int SF_UNIT_BYTES = 4 * SF_BLOCK;    // two stages x (weights, tokens)
 constexpr int SF_COLS = 2 * 2 * KSTEPS * 4;    // two stages of scale columns
 constexpr int MAX_RANKS = 8;                   // the portable cluster size
+constexpr int PER_SM = 2;                      // CTAs per SM
 
 template <int NT>
 struct Cfg {
     static constexpr int X_BYTES = NT * SK / 2;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int PER_SM = NT <= 32 ? 2 : 1;      // CTAs per SM: 97-105 or 193 KB each
-    static constexpr int STAGES = NT <= 32 ? 4 : 7;
+    static constexpr int STAGES = NT <= 32 ? 4 : 3;      // 97-106 KB: two CTAs per SM
     static constexpr int SF_OFF = STAGES * STAGE;
     static constexpr int BAR_OFF = SF_OFF + SF_UNITS * SF_UNIT_BYTES;
     static constexpr int SMEM = BAR_OFF + 256 + 1024;
@@ -1222,8 +1222,20 @@ size_t packed_bytes(int64_t row_blocks, int64_t K)
     return (size_t)row_blocks * (size_t)((K + SK - 1) / SK) * SF_BLOCK;
 }
 
-// The pair kernel takes problems above 128 rows and columns.
-bool use_pair(int64_t M, int64_t N) { return M > 128 && N > 128; }
+// The pair kernel takes what has more than 64 rows and does not fit one wave of
+// the split kernel with two K ranks (148 SMs x 2 CTAs; 64 tokens x 128 columns per
+// tile).  us split / pair: 256 x 256 x 512 3.6 / 5.5, 1024 x 256 x 512 4.0 / 5.8,
+// 512 x 1024 x 4096 9.4 / 10.2, 96 x 8192 x 4096 10.5 / 11.2, 512 x 512 x 16384
+// 12.6 / 23.4, 256 x 256 x 65536 18 / 75, and with 64 rows 64 x 57344 x 4096 33 /
+// 39; but 700 x 1552 x 4096 (143 tiles) 11.5 / 10.5, 320 x 4096 x 4096 (160) 12.7
+// / 11.4, 96 x 28672 x 4096 (448) 25.8 / 23.3, 65536 x 128 x 4096 53 / 42.  Rows of
+// scales on 2-byte boundaries cost the split kernel more, which loads them once
+// per tile: 300 x 1555 x 4128 (65) 12.3 / 13.2, 500 x 1555 x 4128 (104) 16.4 /
+// 13.2, 1000 x 1000 x 1056 (128) 8.2 / 7.6.
+bool use_pair(int64_t M, int64_t N, int64_t K)
+{
+    return M > 64 && (N + 127) / 128 * ((M + 63) / 64) > (K % 64 ? 74 : 148);
+}
 
 template <int BN, int VEC, int ODT>
 int launch_pair(const Problem &p, const DeviceInfo &d)
@@ -1289,33 +1301,40 @@ int launch_pair(const Problem &p, const DeviceInfo &d)
 template <int VEC, int ODT>
 int launch_linear(const Problem &p, const DeviceInfo &d)
 {
-    if (use_pair(p.M, p.N)) {
-        // narrow tiles while each has a pair of SMs of its own
+    if (use_pair(p.M, p.N, p.K)) {
+        // narrow tiles while each has a pair of SMs of its own, or if one spans C
         const int64_t narrow = ((p.M + 2 * duo::PM - 1) / (2 * duo::PM)) * ((p.N + 127) / 128);
-        return narrow <= d.sm_count / 2 ? launch_pair<128, VEC, ODT>(p, d)
-                                        : launch_pair<240, VEC, ODT>(p, d);
+        return narrow <= d.sm_count / 2 || p.N <= 128
+                   ? launch_pair<128, VEC, ODT>(p, d)
+                   : launch_pair<240, VEC, ODT>(p, d);
     }
     if (few::takes(p.M, p.N, p.K))
         return p.M == 1 ? launch_few<1, ODT>(p) : launch_few<2, ODT>(p);
-    // As few tokens per CTA as leave each output tile an SM of its own (32
-    // tokens of 4096 x 4096: 16 per CTA 6.5 us, 32 per CTA 7.2), and the
-    // largest power of two of K ranks that still runs in one wave (a second
-    // wave costs more than all the splitting gains: 32 x 4096 x 4096 6.5 against
+    // The largest power of two of K ranks that still runs in one wave: a second
+    // wave costs more than all the splitting gains (32 x 4096 x 4096 6.5 against
     // 11.4 us).
     const int64_t wt = (p.N + split::WR - 1) / split::WR;
     const int64_t units = (p.K + UNIT - 1) / UNIT;
+    auto tiles = [&](int nt) { return wt * ((p.M + nt - 1) / nt); };
+    const int64_t slots = (int64_t)d.sm_count * split::PER_SM;
     auto run = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        const int64_t tiles = wt * ((p.M + NT - 1) / NT);
-        const int64_t slots = (int64_t)d.sm_count * split::Cfg<NT>::PER_SM;
         int s = 1;
-        while (s < split::MAX_RANKS && 2 * s <= units && tiles * 2 * s <= slots) s *= 2;
+        while (s < split::MAX_RANKS && 2 * s <= units && tiles(NT) * 2 * s <= slots) s *= 2;
         return launch_split<NT, VEC, ODT>(p, d, s);
     };
-    if (p.M <= 16 || wt * ((p.M + 15) / 16) <= d.sm_count)
-        return run(std::integral_constant<int, 16>{});
-    if (p.M <= 32 || wt * ((p.M + 31) / 32) <= d.sm_count)
-        return run(std::integral_constant<int, 32>{});
+    // Few tokens per CTA make the reduction and the epilogue short, many read
+    // the weights fewer times; the tiles' units of K say which counts.  us with 16
+    // / 32 / 64 tokens per CTA: 32 x 4096 x 4096 6.5 / 7.3 / 7.4, 128 x 2048 x 2048
+    // 6.4 / 6.8 / 8.1 (512 units each with 16); 64 x 4096 x 4096 8.1 / 7.7 / 9.4
+    // (1024 with 16), 128 x 8192 x 4096 19.4 / 10.9 / 11.3 (2048 with 32); 128 x
+    // 4096 x 14336 23.5 / 16.9 / 14.0 (3584 with 32), 128 x 14336 x 4096 35.3 /
+    // 20.6 / 12.9.  And one wave whatever K is: 4096 x 256 x 512 8.4 / 4.9 / 6.1.
+    auto suits = [&](int nt, int64_t most) {
+        return p.M <= nt || (tiles(nt) <= slots && tiles(nt) * units <= most);
+    };
+    if (suits(16, 768)) return run(std::integral_constant<int, 16>{});
+    if (suits(32, 2048)) return run(std::integral_constant<int, 32>{});
     return run(std::integral_constant<int, 64>{});
 }
 
@@ -1325,7 +1344,7 @@ extern "C" size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > MAX_MN || N > MAX_MN || K > MAX_K) return 0;
     // the narrowest tile width needs the most blocks
-    return use_pair(M, N) ? packed_bytes((M + 255) / 256 * 2 + (N + 239) / 240 * 2, K) : 0;
+    return use_pair(M, N, K) ? packed_bytes((M + 255) / 256 * 2 + (N + 239) / 240 * 2, K) : 0;
 }
 
 extern "C" int nvfp4_linear(const uint8_t *a_codes, const uint8_t *a_scales, const float *a_ts,

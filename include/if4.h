@@ -371,8 +371,8 @@ int if4_linear_quantized(const uint8_t *a_codes, const uint8_t *a_scales, const 
  * 0), K >= 32, K % 32 == 0 (a row of codes is a whole number of 16-byte
  * units), M and N at most 2^22, K at most 2^20.  a_codes, b_codes 16-byte
  * aligned, a_scales, b_scales 2-byte, C aligned to its element.  workspace
- * (256-byte aligned, nvfp4_linear_workspace_bytes; 0 and NULL for few rows or
- * columns) holds both operands' scales in the tensor cores' order during the
+ * (256-byte aligned, nvfp4_linear_workspace_bytes; 0 and NULL for small
+ * products) holds both operands' scales in the tensor cores' order during the
  * call; calls that may run at the same time need one each.  err_flag must not
  * be NULL (IF4_DEV_BAD_SCALE, IF4_DEV_TIMEOUT).  The pages compare IF4 with NVFP4
  * throughout (gist.science section 4) and name no kernel for it.

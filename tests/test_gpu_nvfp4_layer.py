@@ -41,7 +41,7 @@ def layer_inputs(M, N, K, seed):
     return x, r, wn, w, dy
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (20, 1000, 1056), (160, 320, 288)])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (20, 1000, 1056), (160, 320, 288), (700, 1000, 288)])
 def test_decode_step(M, N, K):
     bb = B()
     x, r, wn, w, _ = layer_inputs(M, N, K, M)
@@ -53,7 +53,7 @@ def test_decode_step(M, N, K):
     close(c, decoded(codes, scales, ts), decoded(*b))
 
 
-@pytest.mark.parametrize("M,N,K", [(96, 160, 224), (256, 384, 512), (320, 288, 1024)])
+@pytest.mark.parametrize("M,N,K", [(96, 160, 224), (256, 384, 512), (320, 288, 1024), (1024, 1280, 1024)])
 def test_training_step(M, N, K):
     bb = B()
     x, r, wn, w, dy = layer_inputs(M, N, K, N)
@@ -78,7 +78,7 @@ def test_training_step(M, N, K):
     assert torch.all((dx.double() - ref).abs() <= 2 ** -8 * ref.abs() + 1e-5 * ref.abs().max())
 
 
-@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("M", [3, 200, 3300])
 def test_captured_step_equals_the_eager_one(M):
     bb = B()
     N, K = 384, 512
@@ -118,7 +118,7 @@ def test_two_streams_at_once():
     bb = B()
     N, K = 512, 1024
     ts = torch.tensor([0.005], device="cuda")
-    sets = [layer_inputs(M, N, K, M) for M in (5, 300)]
+    sets = [layer_inputs(M, N, K, M) for M in (5, 300, 2400)]
     bs = [bb.quantize(s[3], "nvfp4") for s in sets]
 
     def step(s, b):
@@ -129,7 +129,7 @@ def test_two_streams_at_once():
     want = [step(s, b) for s, b in zip(sets, bs)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in sets]
-    got = [[], []]
+    got = [[] for _ in sets]
     for _ in range(4):
         for st, s, b, o in zip(streams, sets, bs, got):
             with torch.cuda.stream(st):
@@ -139,13 +139,13 @@ def test_two_streams_at_once():
         assert all(torch.equal(p, q) for r in o for p, q in zip(r, wnt))
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 2400])
 def test_helpers_on_a_given_stream_share_no_memory_with_the_current_one(M):
     """Work on a side stream that is still waiting, while the current stream
     takes and fills every block that a helper could have returned to it."""
     bb = B()
     N, K = 512, 1024
-    x, r, wn, w, dy = layer_inputs(304, N, K, M)
+    x, r, wn, w, dy = layer_inputs(max(M, 304), N, K, M)
     x, r = x[:M], r[:M]
     ts = torch.tensor([0.005], device="cuda")
     b = bb.quantize(w, "nvfp4")

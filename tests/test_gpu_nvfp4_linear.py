@@ -70,7 +70,13 @@ SIZES = [(1, 1, 32), (1, 16, 32), (3, 7, 96), (1, 4096, 4096), (16, 128, 256), (
          # sizes past the few-token kernel's
          (1, 37, 4128), (2, 129, 1056), (2, 4096, 4096), (1, 8193, 64), (2, 16, 8224),
          # one tile more and fewer than the pairs of SMs
-         (256, 128 * 74, 64), (256, 128 * 75, 64), (512, 241, 544)]
+         (256, 128 * 74, 64), (256, 128 * 75, 64), (512, 241, 544),
+         # CTA pairs: both tile widths, few columns, last tiles of 1 to 16 columns
+         (577, 2177, 64), (650, 1921, 800), (1500, 1700, 512), (4200, 241, 544), (1300, 1937, 256),
+         (20000, 1, 64), (20000, 8, 320), (9990, 30, 1056), (10001, 128, 512), (300, 1936, 4128),
+         # either side of the two kernels' limits
+         (64, 19000, 64), (65, 74 * 128, 128), (65, 74 * 128 + 1, 128), (65, 37 * 128, 96),
+         (65, 37 * 128 + 1, 96)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
@@ -97,7 +103,7 @@ def test_full_workload():
     check(c[rows], (a[0][rows], a[1][rows]), b[:2], a[2], b[2])
 
 
-@pytest.mark.parametrize("M,N", [(5, 200), (200, 384)])
+@pytest.mark.parametrize("M,N", [(5, 200), (200, 384), (700, 1700)])
 def test_operands_from_every_nvfp4_quantizer(M, N):
     bb = B()
     g = torch.Generator().manual_seed(M)
@@ -108,7 +114,8 @@ def test_operands_from_every_nvfp4_quantizer(M, N):
         check(bb.linear_nvfp4(a, b, torch.float32), a[:2], b[:2], a[2], b[2])
 
 
-@pytest.mark.parametrize("M,N,K", [(2, 130, 512), (4, 130, 512), (140, 300, 768)])
+@pytest.mark.parametrize("M,N,K", [(2, 130, 512), (4, 130, 512), (140, 300, 768),
+                                   (600, 2000, 768)])
 def test_all_scales_and_signed_zeros(M, N, K):
     """Every finite E4M3 scale byte, zero included, and every code."""
     g = torch.Generator().manual_seed(K)
@@ -119,7 +126,7 @@ def test_all_scales_and_signed_zeros(M, N, K):
     check(c, a, b, one, one)
 
 
-@pytest.mark.parametrize("M,N", [(2, 256), (8, 256), (256, 256)])
+@pytest.mark.parametrize("M,N", [(2, 256), (8, 256), (256, 256), (640, 1930)])
 def test_nan_scale_stays_in_its_row_and_column(M, N):
     g = torch.Generator().manual_seed(9)
     a, b = operand(M, 512, g), operand(N, 512, g)
@@ -134,7 +141,8 @@ def test_nan_scale_stays_in_its_row_and_column(M, N):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 256, 256), (2, 33, 288), (8, 256, 256), (8, 256, 288),
-                                   (256, 256, 256), (256, 256, 288)])
+                                   (256, 256, 256), (256, 256, 288),
+                                   (640, 1930, 256), (640, 1930, 288)])
 @pytest.mark.parametrize("which", [0, 1])
 def test_int4_groups_are_reported(M, N, K, which):
     g = torch.Generator().manual_seed(9)
@@ -145,7 +153,8 @@ def test_int4_groups_are_reported(M, N, K, which):
     assert int(err) == B().DEV_BAD_SCALE
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 201, 512), (3, 200, 512), (130, 200, 512), (130, 201, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 201, 512), (3, 200, 512), (130, 200, 512), (130, 201, 512),
+                                   (650, 1928, 512), (650, 1921, 512), (9500, 7, 512)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_alignment_and_no_writes_outside(M, N, K, dtype):
     """Scales on a 4-byte boundary only, codes on 16, C on its element's."""
@@ -170,7 +179,8 @@ def test_alignment_and_no_writes_outside(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 100, 96), (2, 100, 512), (9, 100, 96), (9, 100, 512),
-                                   (150, 200, 96), (150, 200, 512), (150, 200, 1056)])
+                                   (150, 200, 96), (150, 200, 512), (150, 200, 1056),
+                                   (600, 2000, 96), (600, 2000, 512), (600, 2000, 1056)])
 def test_rows_of_larger_operands(M, N, K):
     """Views that begin at an odd row: scales on a 2-byte boundary."""
     g = torch.Generator().manual_seed(K)
@@ -191,7 +201,7 @@ def test_empty():
         assert c.shape == (M, N)
 
 
-@pytest.mark.parametrize("M", [1, 300])
+@pytest.mark.parametrize("M", [1, 300, 3300])
 def test_two_graphs_replayed_in_turn(M):
     """Two captured calls that share the error word, each replayed on new data."""
     N, K = 272, 1056
@@ -224,7 +234,7 @@ def test_two_graphs_replayed_in_turn(M):
     assert int(err) == 0
 
 
-@pytest.mark.parametrize("M", [2, 512])
+@pytest.mark.parametrize("M", [2, 512, 1300])
 def test_two_streams_at_once_and_the_same_bits(M):
     N, K = 1024, 2048
     g = torch.Generator().manual_seed(M)
@@ -246,5 +256,6 @@ def test_two_streams_at_once_and_the_same_bits(M):
 def test_an_operand_with_itself():
     bb = B()
     g = torch.Generator().manual_seed(3)
-    a = (*cuda(operand(200, 320, g)), torch.full((1,), 0.01, device="cuda"))
-    check(bb.linear_nvfp4(a, a, torch.float32), a[:2], a[:2], a[2], a[2])
+    for rows in (200, 1300):
+        a = (*cuda(operand(rows, 320, g)), torch.full((1,), 0.01, device="cuda"))
+        check(bb.linear_nvfp4(a, a, torch.float32), a[:2], a[:2], a[2], a[2])

@@ -46,12 +46,12 @@ def test_linear_refusals(lib):
     assert linear(lib, dt=3) == 3 and linear(lib, dt=-1) == 3
     for kw in (dict(ac=A + 8), dict(bc=A + 8), dict(asc=A + 1), dict(bs=A + 1), dict(at=A + 2),
                dict(bt=A + 1), dict(c=A + 1), dict(c=A + 2, dt=0), dict(err=A + 2),
-               dict(M=256, N=256, ws=A + 128)):
+               dict(M=1024, N=1280, ws=A + 128)):
         assert linear(lib, **kw) == 4, kw
-    need = lib.nvfp4_linear_workspace_bytes(256, 256, 64)
+    need = lib.nvfp4_linear_workspace_bytes(1024, 1280, 64)
     assert need > 0
-    assert linear(lib, M=256, N=256, ws=None) == 6
-    assert linear(lib, M=256, N=256, n=need - 1) == 6
+    assert linear(lib, M=1024, N=1280, ws=None) == 6
+    assert linear(lib, M=1024, N=1280, n=need - 1) == 6
 
 
 def test_linear_empty_is_ok(lib):
@@ -61,10 +61,10 @@ def test_linear_empty_is_ok(lib):
 
 def test_linear_workspace(lib):
     f = lib.nvfp4_linear_workspace_bytes
-    assert f(1, 4096, 4096) == 0 and f(4096, 16, 64) == 0     # few rows, few columns
+    assert f(1, 4096, 4096) == 0 and f(64, 1 << 20, 64) == 0 and f(256, 256, 64) == 0
     # blocks of 128 rows x 16 scales: two per 256 rows of A, two per 240 of B
-    assert f(256, 480, 256) == (2 + 4) * 2048
-    assert f(257, 481, 288) == (4 + 6) * 2 * 2048             # rows and K rounded up
+    assert f(1024, 1440, 256) == (8 + 12) * 2048
+    assert f(1025, 1441, 288) == (10 + 14) * 2 * 2048         # rows and K rounded up
     for bad in ((0, 4, 64), (4, 0, 64), (4, 4, 16), (4, 4, 40), (1 << 23, 4, 64)):
         assert f(*bad) == 0
 
