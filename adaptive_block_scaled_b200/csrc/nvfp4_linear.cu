@@ -323,7 +323,7 @@ nvfp4_linear_few(const uint8_t *x_codes, const uint8_t *x_scales, const float *x
     if ((bad & 0x8080u) && err) atomicOr(err, IF4_DEV_BAD_SCALE);
 }
 
-// ------------------------------------------------- few rows: split over K ----
+// -------------------------------------------- small products: split over K ----
 //
 // Few tokens, or few output tiles.  The weight rows take the MMA's M side (128
 // per CTA) and NT tokens its N side, so D is C transposed: a lane holds one
@@ -332,6 +332,11 @@ nvfp4_linear_few(const uint8_t *x_codes, const uint8_t *x_scales, const float *x
 // its shared memory, and the CTAs add the S partials in rank order through
 // distributed shared memory, each for its share of the tokens: no workspace,
 // no atomics, the same sum every time.
+//
+// About 3.5 us of it is launch, tensor memory and the first loads' latency, 1.2
+// the reduction, and the rest the operands' way from L2, at about 8 TB/s: 256 x
+// 256 x 512 3.6 us, 48 x 8192 x 4096 9.2, 100 x 4096 x 14336 14.9.  (Scales loaded
+// two, three or four units ahead instead of one: 1 to 10 % slower.)
 
 namespace split {
 
