@@ -335,7 +335,7 @@ nvfp4_linear_few(const uint8_t *x_codes, const uint8_t *x_scales, const float *x
 //
 // About 3.5 us of it is launch, tensor memory and the first loads' latency, 1.2
 // the reduction, and the rest the operands' way from L2, at about 8 TB/s: 256 x
-// 256 x 512 3.6 us, 48 x 8192 x 4096 8.7, 100 x 4096 x 14336 14.9.  (Scales loaded
+// 256 x 512 3.6 us, 48 x 8192 x 4096 9.2, 100 x 4096 x 14336 14.9.  (Scales loaded
 // two, three or four units ahead instead of one: 1 to 10 % slower.)
 
 namespace split {
@@ -1335,14 +1335,11 @@ int launch_linear(const Problem &p, const DeviceInfo &d)
     // (1024 with 16), 128 x 8192 x 4096 19.4 / 10.9 / 11.3 (2048 with 32); 128 x
     // 4096 x 14336 23.5 / 16.9 / 14.0 (3584 with 32), 128 x 14336 x 4096 35.3 /
     // 20.6 / 12.9.  And one wave whatever K is: 4096 x 256 x 512 8.4 / 4.9 / 6.1.
-    // Where 32 would leave half of the second tile empty, 64 is ahead sooner: 48 x
-    // 8192 x 4096 9.6 / 9.1 / 8.6 (1024), 40 x 4096 x 14336 14.7 / 11.6 / 11.0 (1792),
-    // but 48 x 4096 x 4096 7.6 / 7.6 / 8.3 (512).
     auto suits = [&](int nt, int64_t most) {
         return p.M <= nt || (tiles(nt) <= slots && tiles(nt) * units <= most);
     };
     if (suits(16, 768)) return run(std::integral_constant<int, 16>{});
-    if (suits(32, p.M > 32 && p.M <= 48 ? 768 : 2048)) return run(std::integral_constant<int, 32>{});
+    if (suits(32, 2048)) return run(std::integral_constant<int, 32>{});
     return run(std::integral_constant<int, 64>{});
 }
 
