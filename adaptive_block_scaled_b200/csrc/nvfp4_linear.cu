@@ -1227,19 +1227,22 @@ size_t packed_bytes(int64_t row_blocks, int64_t K)
     return (size_t)row_blocks * (size_t)((K + SK - 1) / SK) * SF_BLOCK;
 }
 
-// The pair kernel takes what has more than 64 rows and does not fit one wave of
-// the split kernel with two K ranks (148 SMs x 2 CTAs; 64 tokens x 128 columns per
-// tile).  us split / pair: 256 x 256 x 512 3.6 / 5.5, 1024 x 256 x 512 4.0 / 5.8,
-// 512 x 1024 x 4096 9.4 / 10.2, 96 x 8192 x 4096 10.5 / 11.2, 512 x 512 x 16384
-// 12.6 / 23.4, 256 x 256 x 65536 18 / 75, and with 64 rows 64 x 57344 x 4096 33 /
-// 39; but 700 x 1552 x 4096 (143 tiles) 11.5 / 10.5, 320 x 4096 x 4096 (160) 12.7
-// / 11.4, 96 x 28672 x 4096 (448) 25.8 / 23.3, 65536 x 128 x 4096 53 / 42.  Rows of
-// scales on 2-byte boundaries cost the split kernel more, which loads them once
-// per tile: 300 x 1555 x 4128 (65) 12.3 / 13.2, 500 x 1555 x 4128 (104) 16.4 /
-// 13.2, 1000 x 1000 x 1056 (128) 8.2 / 7.6.
+// The pair kernel takes what has more than 64 rows and more tiles of 64 tokens x
+// 128 columns than the split kernel runs at once (148 SMs x 2 CTAs; above 128
+// rows, which fill a pair's tile, with two K ranks).  us split / pair, weights
+// from memory: 128 x 2048 x 2048 6.5 / 8.4, 512 x 1024 x 4096 9.2 / 10.6, 128 x
+// 14336 x 4096 (224 tiles) 14.0 / 15.1, 256 x 4096 x 4096 (128) 10.7 / 11.2, 256 x
+// 4096 x 14336 20.3 / 23.5, and with 64 rows 64 x 28672 x 4096 17.8 / 23.5; from L2
+// 256 x 256 x 512 3.6 / 5.5, 512 x 512 x 16384 12.6 / 23.4, 256 x 256 x 65536 18 /
+// 75; but 320 x 4096 x 4096 (160) 12.7 / 11.4, 160 x 8192 x 4096 (192) 12.7 / 11.4,
+// 96 x 28672 x 4096 (448) 26.5 / 23.9, 65536 x 128 x 4096 53 / 42.  Rows of scales
+// on 2-byte boundaries cost the split kernel more, which loads them once per
+// tile: 300 x 1555 x 4128 (65) 12.3 / 13.2, 500 x 1555 x 4128 (104) 16.4 / 13.2,
+// 1000 x 1000 x 1056 (128) 8.2 / 7.6.
 bool use_pair(int64_t M, int64_t N, int64_t K)
 {
-    return M > 64 && (N + 127) / 128 * ((M + 63) / 64) > (K % 64 ? 74 : 148);
+    const int64_t most = (M <= 128 ? 296 : 148) / (K % 64 ? 2 : 1);
+    return M > 64 && (N + 127) / 128 * ((M + 63) / 64) > most;
 }
 
 template <int BN, int VEC, int ODT>

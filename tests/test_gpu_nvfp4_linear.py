@@ -75,8 +75,9 @@ SIZES = [(1, 1, 32), (1, 16, 32), (3, 7, 96), (1, 4096, 4096), (16, 128, 256), (
          (577, 2177, 64), (650, 1921, 800), (1500, 1700, 512), (4200, 241, 544), (1300, 1937, 256),
          (20000, 1, 64), (20000, 8, 320), (9990, 30, 1056), (10001, 128, 512), (300, 1936, 4128),
          # either side of the two kernels' limits
-         (64, 19000, 64), (65, 74 * 128, 128), (65, 74 * 128 + 1, 128), (65, 37 * 128, 96),
-         (65, 37 * 128 + 1, 96)]
+         (64, 19000, 64), (65, 148 * 128, 128), (128, 148 * 128 + 1, 128), (65, 74 * 128, 96),
+         (65, 74 * 128 + 1, 96), (129, 49 * 128, 128), (129, 49 * 128 + 1, 128),
+         (40, 8200, 4096), (48, 4100, 14432), (33, 14400, 2080)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
