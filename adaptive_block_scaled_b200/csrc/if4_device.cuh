@@ -277,15 +277,40 @@ __device__ __forceinline__ void pdl_release()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// A float that an earlier kernel of the stream may have written.  Read this
-// way it stays behind pdl_enter(): the compiler takes a load through a const
-// __restrict__ pointer for one of memory that never changes, and may move it
-// in front of the wait.
+// Loads of what an earlier kernel of the stream may have written, for use after
+// pdl_enter().  Read this way they stay behind the wait and see what it made
+// visible: the compiler takes a load through a const __restrict__ pointer, and
+// the hardware an ld.global.nc, for one of memory that never changes while the
+// kernel runs.  The compiler may move such a load in front of the wait, and
+// the hardware may serve it from a line that a kernel still running on the SM
+// brought into L1 before the wait.  (A producer two launches back is covered
+// too: every kernel waits for the one before it.)
 __device__ __forceinline__ float ld_after_wait(const float *p)
 {
     float v;
     asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
     return v;
+}
+
+__device__ __forceinline__ uint32_t ld_after_wait_u32(const void *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_after_wait_u16(const void *p)
+{
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void ld_after_wait_v4(const void *p, uint32_t &a, uint32_t &b,
+                                                 uint32_t &c, uint32_t &d)
+{
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
 }
 
 // Wall clock in nanoseconds, for bounded waits.

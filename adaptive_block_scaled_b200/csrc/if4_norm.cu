@@ -157,16 +157,14 @@ __device__ __forceinline__ void zero_group(Raw<DT> &r)
     for (uint32_t &w : r.w) w = 0u;
 }
 
-// A group of the weight, kept in L1 for the next rows.
+// A group of the weight (L1 keeps it for the next rows).
 template <int WT>
 __device__ __forceinline__ void load_weight(const char *w, int g, Raw<WT> &r)
 {
     const char *p = w + (int64_t)g * 16 * elem_bytes<WT>();
 #pragma unroll
     for (int q = 0; q < (WT == DT_F32 ? 4 : 2); ++q)
-        asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-            : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
-            : "l"(p + 16 * q));
+        ld_after_wait_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
 }
 
 // h = RN(x + r), into x.  16-bit types add in their own type: the sum of two
@@ -549,10 +547,8 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
         if (u < units) {
 #pragma unroll
             for (int q = 0; q < (WT == DT_F32 ? 2 : 1); ++q)
-                asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                    : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]),
-                      "=r"(r.w[4 * q + 3])
-                    : "l"(a.w + (int64_t)u * Unit<WT>::BYTES + 16 * q));
+                ld_after_wait_v4(a.w + (int64_t)u * Unit<WT>::BYTES + 16 * q, r.w[4 * q],
+                                 r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
         }
         return r;
     };

@@ -126,14 +126,11 @@ __device__ __forceinline__ void load_scales16(const uint8_t *p, int nb, uint32_t
 {
     w[0] = w[1] = w[2] = w[3] = 0u;
     if constexpr (VEC == 16) {
-        if (nb > 0)
-            asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+        if (nb > 0) ld_after_wait_v4(p, w[0], w[1], w[2], w[3]);
     } else if constexpr (VEC == 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (nb > 4 * j)
-                asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[j]) : "l"(p + 4 * j));
+            if (nb > 4 * j) w[j] = ld_after_wait_u32(p + 4 * j);
     } else if (nb >= 16) {
         // rows on 4-byte and on 2-byte boundaries in turn: the aligned words
         // that hold the 16 bytes (the first may begin in the row before), the
@@ -141,23 +138,16 @@ __device__ __forceinline__ void load_scales16(const uint8_t *p, int nb, uint32_t
         const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 2u;
         uint32_t a[5];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(a[j]) : "l"(p - off + 4 * j));
-        uint16_t last = 0;
-        if (off) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(last) : "l"(p + 14));
-        a[4] = last;
+        for (int j = 0; j < 4; ++j) a[j] = ld_after_wait_u32(p - off + 4 * j);
+        a[4] = off ? ld_after_wait_u16(p + 14) : 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(a[j], a[j + 1], 8 * off);
     } else {
-        uint16_t h[8];
+        uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            h[j] = 0;
-            if (nb > 2 * j)
-                asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h[j]) : "l"(p + 2 * j));
-        }
+        for (int j = 0; j < 8; ++j) h[j] = nb > 2 * j ? ld_after_wait_u16(p + 2 * j) : 0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)h[2 * j] | (uint32_t)h[2 * j + 1] << 16;
+        for (int j = 0; j < 4; ++j) w[j] = h[2 * j] | h[2 * j + 1] << 16;
     }
 }
 
@@ -251,13 +241,8 @@ nvfp4_linear_few(const uint8_t *x_codes, const uint8_t *x_scales, const float *x
                     uint32_t (&w)[4], uint32_t &s) {
         w[0] = w[1] = w[2] = w[3] = s = 0u;
         if (in) {
-            asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "l"(codes + row * cb + (int64_t)piece * 16));
-            uint16_t h;
-            asm volatile("ld.global.nc.u16 %0, [%1];"
-                         : "=h"(h) : "l"(scales + row * sb + (int64_t)piece * 2));
-            s = h;
+            ld_after_wait_v4(codes + row * cb + (int64_t)piece * 16, w[0], w[1], w[2], w[3]);
+            s = ld_after_wait_u16(scales + row * sb + (int64_t)piece * 2);
         }
     };
     for (int p0 = lane; p0 < pieces; p0 += 32 * CHUNK) {

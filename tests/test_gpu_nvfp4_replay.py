@@ -1,0 +1,66 @@
+"""Kernels that start early, run over the same buffers again and again: each
+round rewrites the operands that the round before has read."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def B():
+    from adaptive_block_scaled_b200 import binding
+    return binding
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("M", [1, 2, 48, 300])
+@pytest.mark.parametrize("N,K", [(256, 512), (2048, 2048), (1032, 1056)])
+def test_norm_and_product_over_the_same_buffers(M, N, K, captured):
+    bb = B()
+    g = torch.Generator().manual_seed(M + N)
+    rounds = 12
+    xs = [torch.randn((M, K), generator=g).bfloat16().cuda() for _ in range(rounds)]
+    ws = [(0.02 * torch.randn((N, K), generator=g)).bfloat16().cuda() for _ in range(rounds)]
+    wn = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    ts = torch.tensor([0.004], device="cuda")
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    codes, scales = torch.empty((M, K // 2), **u8), torch.empty((M, K // 16), **u8)
+    wc, wsc, wts = torch.empty((N, K // 2), **u8), torch.empty((N, K // 16), **u8), \
+        torch.tensor([1e-4], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    need = bb.nvfp4_linear_workspace_bytes(M, N, K)
+    work = torch.empty(need, **u8) if need else None
+    outs = [torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(rounds)]
+
+    def run():
+        # one round: the activations' and the weight's codes rewritten, then read;
+        # the next round's norm may start under this round's product
+        for x, w, c in zip(xs, ws, outs):
+            bb.nvfp4_quantize(w, wc, wsc, wts, bb.TS_GIVEN)
+            bb.nvfp4_rms_norm_quantize(x, None, wn, 1e-6, None, None, codes, scales, ts)
+            bb.nvfp4_linear(codes, scales, ts, wc, wsc, wts, work, c, err)
+            bb.nvfp4_rms_norm_quantize(x[:1], None, wn, 1e-6, None, None, codes[:1], scales[:1], ts)
+
+    want = []
+    for x, w in zip(xs, ws):
+        q = bb.quantize(w, "nvfp4", ts=wts)
+        a = bb.rms_norm_quantize(x, wn, ts, mode="nvfp4")
+        torch.cuda.synchronize()
+        want.append(bb.linear_nvfp4((a[0], a[1], ts), q))
+        torch.cuda.synchronize()
+    run()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(4):
+        for c in outs:
+            c.zero_()
+        if captured:
+            graph.replay()
+        else:
+            run()
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        for c, k in zip(outs, want):
+            assert torch.equal(c, k)
