@@ -33,7 +33,7 @@ SOURCES = [
     ("ifw_quant.cu", ["-fmad=false"]),    # IF6 / IF3: the same arithmetic contract
 ]
 HEADERS = ["if4_device.cuh", "if4_encode.cuh", "if4_decode.cuh", "if4_internal.h", "if4_tc.cuh",
-           "if4_load.cuh", "if4_host.cuh", "exports.map"]
+           "if4_load.cuh", "if4_host.cuh", "nvfp4_scales.cuh", "exports.map"]
 
 
 def _nvcc():

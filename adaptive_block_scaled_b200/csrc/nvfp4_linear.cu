@@ -32,6 +32,7 @@
 #include "if4_device.cuh"
 #include "if4_host.cuh"
 #include "if4_tc.cuh"
+#include "nvfp4_scales.cuh"
 
 namespace {
 
@@ -118,37 +119,21 @@ __device__ __forceinline__ void fence_async_smem()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// The 16 scale bytes at p, of which the first nb exist (nb <= 0: none); the
-// others read as 0.  VEC: the bytes that p's and nb's alignment allows per
-// load: 16 (K % 256 == 0, aligned base), 4 (K % 64 == 0, aligned base) or 2.
+// Loader of load_scales16: behind the launch wait.
+struct AfterWait {
+    __device__ __forceinline__ uint32_t u16(const uint8_t *p) const { return ld_after_wait_u16(p); }
+    __device__ __forceinline__ uint32_t u32(const uint8_t *p) const { return ld_after_wait_u32(p); }
+    __device__ __forceinline__ void v4(const uint8_t *p, uint32_t &a, uint32_t &b, uint32_t &c,
+                                       uint32_t &d) const
+    {
+        ld_after_wait_v4(p, a, b, c, d);
+    }
+};
+
 template <int VEC>
 __device__ __forceinline__ void load_scales16(const uint8_t *p, int nb, uint32_t (&w)[4])
 {
-    w[0] = w[1] = w[2] = w[3] = 0u;
-    if constexpr (VEC == 16) {
-        if (nb > 0) ld_after_wait_v4(p, w[0], w[1], w[2], w[3]);
-    } else if constexpr (VEC == 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (nb > 4 * j) w[j] = ld_after_wait_u32(p + 4 * j);
-    } else if (nb >= 16) {
-        // rows on 4-byte and on 2-byte boundaries in turn: the aligned words
-        // that hold the 16 bytes (the first may begin in the row before), the
-        // last two bytes by themselves, shifted together
-        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 2u;
-        uint32_t a[5];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = ld_after_wait_u32(p - off + 4 * j);
-        a[4] = off ? ld_after_wait_u16(p + 14) : 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(a[j], a[j + 1], 8 * off);
-    } else {
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = nb > 2 * j ? ld_after_wait_u16(p + 2 * j) : 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = h[2 * j] | h[2 * j + 1] << 16;
-    }
+    load_scales16<VEC>(p, nb, w, AfterWait());
 }
 
 // One accumulator value to its output type.

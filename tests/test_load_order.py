@@ -26,7 +26,7 @@ def test_no_load_that_takes_memory_for_constant(name):
     assert "ld.global.nc" not in text and "__ldg" not in text
 
 
-@pytest.mark.parametrize("name", FILES + ["if4_tc.cuh"])
+@pytest.mark.parametrize("name", FILES + ["if4_tc.cuh", "nvfp4_scales.cuh"])
 def test_every_load_instruction_keeps_its_place(name):
     text = code(name)
     for m in re.finditer(r'asm\s*(volatile)?\s*\(\s*"((?:[^"\\]|\\.)*)"', text):
