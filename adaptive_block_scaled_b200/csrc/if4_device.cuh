@@ -9,46 +9,78 @@ namespace if4dev {
 
 // ------------------------------------------------------------ memory ----
 
-// 256-bit read-only load, not kept in L1 (every byte is read once).
-__device__ __forceinline__ void ld_nc_v8(const void *p, uint32_t (&r)[8])
+// Loads of what an earlier kernel of the stream may have written, for use after
+// the launch wait (pdl_enter).  They are volatile and coherent, so that they
+// stay behind the wait and see what it made visible: the compiler takes a load
+// through a const __restrict__ pointer, and the hardware an ld.global.nc, for
+// one of memory that never changes while the kernel runs.  The compiler may move
+// such a load in front of the wait, and the hardware may serve it from a line
+// that a kernel still running on the SM brought into L1 before the wait.  (A
+// producer two launches back is covered too: every kernel waits for the one
+// before it.)
+
+// 256 bits, not kept in L1 (every byte is read once); likewise the next three.
+__device__ __forceinline__ void ld_v8(const void *p, uint32_t (&r)[8])
 {
-    asm("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]),
-          "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]),
+                   "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
 }
 
-__device__ __forceinline__ void ld_nc_v4(const void *p, uint32_t &a, uint32_t &b,
-                                         uint32_t &c, uint32_t &d)
+__device__ __forceinline__ void ld_v4(const void *p, uint32_t &a, uint32_t &b, uint32_t &c,
+                                      uint32_t &d)
 {
-    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
 }
 
-__device__ __forceinline__ void ld_nc_v2(const void *p, uint32_t &a, uint32_t &b)
+__device__ __forceinline__ void ld_v2(const void *p, uint32_t &a, uint32_t &b)
 {
-    asm("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "l"(p));
 }
 
-__device__ __forceinline__ uint32_t ld_nc_u32(const void *p)
+__device__ __forceinline__ uint32_t ld_u8(const void *p)
+{
+    uint16_t v;
+    asm volatile("ld.global.L1::no_allocate.u8 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+// The same, kept in L1: values that several lanes, rows or blocks share.
+__device__ __forceinline__ float ld_after_wait(const float *p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_after_wait_u32(const void *p)
 {
     uint32_t v;
-    asm("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 
-__device__ __forceinline__ uint32_t ld_nc_u16(const void *p)
+__device__ __forceinline__ uint32_t ld_after_wait_u16(const void *p)
 {
     uint16_t v;
-    asm("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 
-__device__ __forceinline__ uint32_t ld_nc_u8(const void *p)
+__device__ __forceinline__ uint32_t ld_after_wait_u8(const void *p)
 {
     uint16_t v;
-    asm("ld.global.nc.L1::no_allocate.u8 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.u8 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
+}
+
+__device__ __forceinline__ void ld_after_wait_v4(const void *p, uint32_t &a, uint32_t &b,
+                                                 uint32_t &c, uint32_t &d)
+{
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
 }
 
 // --------------------------------------------- L2 eviction priority ----
@@ -77,18 +109,18 @@ __device__ __forceinline__ uint64_t l2_evict_last()
     return p;
 }
 
-__device__ __forceinline__ void ld_nc_v8_pol(const void *p, uint32_t (&r)[8], uint64_t pol)
+__device__ __forceinline__ void ld_v8_pol(const void *p, uint32_t (&r)[8], uint64_t pol)
 {
-    asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]),
           "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "l"(p), "l"(pol));
 }
 
-__device__ __forceinline__ void ld_nc_v4_pol(const void *p, uint32_t &a, uint32_t &b, uint32_t &c,
-                                             uint32_t &d, uint64_t pol)
+__device__ __forceinline__ void ld_v4_pol(const void *p, uint32_t &a, uint32_t &b, uint32_t &c,
+                                          uint32_t &d, uint64_t pol)
 {
-    asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;"
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;"
         : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p), "l"(pol));
 }
 
@@ -275,42 +307,6 @@ __device__ __forceinline__ void pdl_enter()
 __device__ __forceinline__ void pdl_release()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Loads of what an earlier kernel of the stream may have written, for use after
-// pdl_enter().  Read this way they stay behind the wait and see what it made
-// visible: the compiler takes a load through a const __restrict__ pointer, and
-// the hardware an ld.global.nc, for one of memory that never changes while the
-// kernel runs.  The compiler may move such a load in front of the wait, and
-// the hardware may serve it from a line that a kernel still running on the SM
-// brought into L1 before the wait.  (A producer two launches back is covered
-// too: every kernel waits for the one before it.)
-__device__ __forceinline__ float ld_after_wait(const float *p)
-{
-    float v;
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint32_t ld_after_wait_u32(const void *p)
-{
-    uint32_t v;
-    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t ld_after_wait_u16(const void *p)
-{
-    uint16_t v;
-    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ void ld_after_wait_v4(const void *p, uint32_t &a, uint32_t &b,
-                                                 uint32_t &c, uint32_t &d)
-{
-    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
 }
 
 // Wall clock in nanoseconds, for bounded waits.

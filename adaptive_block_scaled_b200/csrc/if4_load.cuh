@@ -23,21 +23,21 @@ __device__ __forceinline__ void load_group(const char *p, Raw<DT> &r)
     if constexpr (DT == DT_F32) {
         if constexpr (V8) {
             uint32_t a[8], b[8];
-            ld_nc_v8(p, a);
-            ld_nc_v8(p + 32, b);
+            ld_v8(p, a);
+            ld_v8(p + 32, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) { r.w[i] = a[i]; r.w[8 + i] = b[i]; }
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                ld_nc_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
+                ld_v4(p + 16 * q, r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
         }
     } else {
         if constexpr (V8) {
-            ld_nc_v8(p, r.w);
+            ld_v8(p, r.w);
         } else {
-            ld_nc_v4(p, r.w[0], r.w[1], r.w[2], r.w[3]);
-            ld_nc_v4(p + 16, r.w[4], r.w[5], r.w[6], r.w[7]);
+            ld_v4(p, r.w[0], r.w[1], r.w[2], r.w[3]);
+            ld_v4(p + 16, r.w[4], r.w[5], r.w[6], r.w[7]);
         }
     }
 }

@@ -144,7 +144,7 @@ __device__ __forceinline__ void load16(const char *p, float (&x)[16], float &ama
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t a, b, c, d;
-            ld_nc_v4(p + 16 * q, a, b, c, d);
+            ld_v4(p + 16 * q, a, b, c, d);
             x[4 * q] = __uint_as_float(a);
             x[4 * q + 1] = __uint_as_float(b);
             x[4 * q + 2] = __uint_as_float(c);
@@ -160,8 +160,8 @@ __device__ __forceinline__ void load16(const char *p, float (&x)[16], float &ama
         }
     } else {
         uint32_t w[8];
-        ld_nc_v4(p, w[0], w[1], w[2], w[3]);
-        ld_nc_v4(p + 16, w[4], w[5], w[6], w[7]);
+        ld_v4(p, w[0], w[1], w[2], w[3]);
+        ld_v4(p + 16, w[4], w[5], w[6], w[7]);
         words16<DT>(w, x, amax, nonfinite);
     }
 }
@@ -233,15 +233,13 @@ template <int BITS>
 __device__ __forceinline__ void load_code_words(const uint8_t *p, uint32_t (&w)[3])
 {
     if constexpr (BITS == 6) {
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-        w[0] = __ldg(q);
-        w[1] = __ldg(q + 1);
-        w[2] = __ldg(q + 2);
+        w[0] = ld_after_wait_u32(p);
+        w[1] = ld_after_wait_u32(p + 4);
+        w[2] = ld_after_wait_u32(p + 8);
     } else {
-        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
-        w[0] = __ldg(q);
-        w[1] = __ldg(q + 1);
-        w[2] = __ldg(q + 2);
+        w[0] = ld_after_wait_u16(p);
+        w[1] = ld_after_wait_u16(p + 2);
+        w[2] = ld_after_wait_u16(p + 4);
     }
 }
 
@@ -575,8 +573,8 @@ ifw_quantize_kernel(const char *__restrict__ x, int64_t ld_bytes, uint32_t gpr, 
     if constexpr (PF) {
         if (g0 < ngroups) {
             const char *p0 = gaddr(g0);
-            ld_nc_v4(p0, wn[0], wn[1], wn[2], wn[3]);
-            ld_nc_v4(p0 + 16, wn[4], wn[5], wn[6], wn[7]);
+            ld_v4(p0, wn[0], wn[1], wn[2], wn[3]);
+            ld_v4(p0 + 16, wn[4], wn[5], wn[6], wn[7]);
         }
     }
     for (uint32_t g = g0; g < ngroups; g += stride) {
@@ -588,8 +586,8 @@ ifw_quantize_kernel(const char *__restrict__ x, int64_t ld_bytes, uint32_t gpr, 
             words16<DT>(wn, xv, amax, nf);
             if (g + stride < ngroups) {
                 const char *pn = gaddr(g + stride);
-                ld_nc_v4(pn, wn[0], wn[1], wn[2], wn[3]);
-                ld_nc_v4(pn + 16, wn[4], wn[5], wn[6], wn[7]);
+                ld_v4(pn, wn[0], wn[1], wn[2], wn[3]);
+                ld_v4(pn + 16, wn[4], wn[5], wn[6], wn[7]);
             }
         } else {
             load16<DT>(p, xv, amax, nf);
@@ -681,7 +679,7 @@ ifw_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restri
     uint32_t w[3] = {0u, 0u, 0u}, sbn = 0u;
     if (g0 < ngroups) {
         load_code_words<BITS>(codes + (int64_t)g0 * CB, w);
-        sbn = __ldg(scales + g0);
+        sbn = ld_after_wait_u8(scales + g0);
     }
     for (uint32_t g = g0; g < ngroups; g += stride) {
         uint32_t c[16];
@@ -689,7 +687,7 @@ ifw_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restri
         const uint32_t sb = sbn;
         if (g + stride < ngroups) {
             load_code_words<BITS>(codes + (int64_t)(g + stride) * CB, w);
-            sbn = __ldg(scales + g + stride);
+            sbn = ld_after_wait_u8(scales + g + stride);
         }
         const float eff = __fmul_rn(f32_from_e4m3(sb & 0x7Fu), ts);
         const float *tab = (sb & 0x80u) ? int_tab : fp_tab;

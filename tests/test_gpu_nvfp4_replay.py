@@ -64,3 +64,54 @@ def test_norm_and_product_over_the_same_buffers(M, N, K, captured):
         assert int(err) == 0
         for c, k in zip(outs, want):
             assert torch.equal(c, k)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 256), (64, 512), (512, 2048)])
+def test_quantizers_and_dequantizers_over_the_same_buffers(rows, cols, captured):
+    """quantize -> dequantize (IF4, IF6, IF3) in place of the input, round after
+    round: every kernel reads what the one before it wrote."""
+    bb = B()
+    g = torch.Generator().manual_seed(rows + cols)
+    rounds = 12
+    xs = [torch.randn((rows, cols), generator=g).bfloat16().cuda() for _ in range(rounds)]
+    ts = torch.tensor([0.002], device="cuda")
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    codes = {b: torch.empty((rows, cols * b // 8), **u8) for b in (4, 6, 3)}
+    scales = torch.empty((rows, cols // 16), **u8)
+    buf = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    outs = [torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda") for _ in range(rounds)]
+
+    def run(sync=lambda: None):
+        for x, out in zip(xs, outs):
+            src = x
+            for bits, dst in ((4, buf), (6, buf), (3, out)):
+                if bits == 4:
+                    bb.if4_quantize(src, codes[4], scales, ts, bb.TS_COMPUTE)
+                    sync()
+                    bb.if4_dequantize(codes[4], scales, ts, dst)
+                else:
+                    bb.ifw_quantize(src, bits, bb.W_ADAPTIVE, codes[bits], scales, ts, bb.TS_COMPUTE)
+                    sync()
+                    bb.ifw_dequantize(codes[bits], scales, ts, bits, dst)
+                sync()
+                src = buf
+
+    run(torch.cuda.synchronize)
+    want = [o.clone() for o in outs]
+    run()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        if captured:
+            graph.replay()
+        else:
+            run()
+        torch.cuda.synchronize()
+        for o, k in zip(outs, want):
+            assert torch.equal(o, k)

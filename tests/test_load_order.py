@@ -12,7 +12,8 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "adaptive_block_scaled_b200", "csrc")
-FILES = ["nvfp4_linear.cu", "if4_norm.cu", "if4_quant_t.cu"]
+FILES = ["nvfp4_linear.cu", "if4_norm.cu", "if4_quant_t.cu", "if4_quant.cu", "ifw_quant.cu",
+         "if4_linear.cu", "if4_device.cuh", "if4_load.cuh", "if4_encode.cuh", "if4_decode.cuh"]
 
 
 def code(name):
