@@ -1,0 +1,149 @@
+"""Which device and stream the binding's calls run on (no GPU needed: the C
+calls and the device lookup are replaced)."""
+import contextlib
+
+import pytest
+import torch
+
+U8, F32, BF16 = torch.uint8, torch.float32, torch.bfloat16
+
+
+def z(*shape, dtype=U8):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def entries(b):
+    """name -> a call of that entry point with every tensor on the CPU."""
+    x, ts, err = z(32, 64, dtype=BF16), z(1, dtype=F32), z(1, dtype=torch.int32)
+    c, s, sync = z(32, 32), z(32, 4), z(64, dtype=torch.int32)
+    y, h = z(32, 64, dtype=BF16), z(32, 64, dtype=torch.float16)
+    w = z(1 << 20)
+    wc, ws, o = z(64, 32), z(64, 4), z(32, 64, dtype=BF16)
+    op = (c, s, ts, wc, ws, ts)
+    calls = {
+        "if4_tensor_amax": lambda **k: b.if4_tensor_amax(x, ts, err, **k),
+        "if4_tensor_scale": lambda **k: b.if4_tensor_scale(ts, ts, **k),
+        "if4_tensor_amax_rht": lambda **k: b.if4_tensor_amax_rht(x, 5, ts, err, **k),
+        "if4_quantize_rht": lambda **k: b.if4_quantize_rht(x, 5, c, s, ts, 0, err, **k),
+        "if4_quantize_fused": lambda **k: b.if4_quantize_fused(x, c, s, None, None, ts, sync, err, **k),
+        "if4_quantize_fused_rht":
+            lambda **k: b.if4_quantize_fused(x, c, s, c, s, ts, sync, err, signs=3, **k),
+        "if4_quantize_fused_shared":
+            lambda **k: b.if4_quantize_fused_shared(x, c, s, None, None, ts, sync, 2, err, **k),
+        "if4_quantize_fused_rht_shared":
+            lambda **k: b.if4_quantize_fused_shared(x, c, s, c, s, ts, sync, 2, err, signs=3, **k),
+        "if4_quantize_fused_dequant":
+            lambda **k: b.if4_quantize_fused_dequant(x, c, s, None, None, ts, sync, y, err, **k),
+        "if4_quantize_fused_dequant_shared":
+            lambda **k: b.if4_quantize_fused_dequant_shared(x, c, s, c, s, ts, sync, y, 2, err, **k),
+        "if4_dequantize": lambda **k: b.if4_dequantize(c, s, ts, y, **k),
+        "if4_decode_f16": lambda **k: b.if4_decode_f16(c, s, h, **k),
+        "if4_gemm_f16": lambda **k: b.if4_gemm_f16(h, z(64, 64, dtype=torch.float16), ts, ts, o, err, **k),
+        "if4_linear": lambda **k: b.if4_linear(*op, w, o, err, **k),
+        "if4_linear_fused": lambda **k: b.if4_linear_fused(*op, o, err, **k),
+        "if4_linear_noalloc": lambda **k: b.if4_linear_noalloc(*op, o, err, **k),
+        "if4_linear_quantized": lambda **k: b.if4_linear_quantized(*op, w, c, s, ts, o, err, **k),
+        "nvfp4_linear": lambda **k: b.nvfp4_linear(*op, None, o, err, **k),
+        "if4_rms_norm_backward":
+            lambda **k: b.if4_rms_norm_backward(y, y, z(64, dtype=F32), z(32, dtype=F32), None, y,
+                                                z(64, dtype=F32), w, **k),
+    }
+    for n in ("if4_quantize", "nvfp4_quantize", "nvint4_quantize", "nvfp4_4over6_quantize"):
+        calls[n] = lambda n=n, **k: getattr(b, n)(x, c, s, ts, 0, err, **k)
+    for n in ("if4_quantize_t", "nvfp4_quantize_t"):
+        calls[n] = lambda n=n, **k: getattr(b, n)(x, c, s, z(64, 16), z(64, 2), ts, 0, err, **k)
+    for n in ("if4_rms_norm_quantize", "nvfp4_rms_norm_quantize"):
+        calls[n] = lambda n=n, **k: getattr(b, n)(x, None, z(64, dtype=F32), 1e-6, None, None, c, s,
+                                                  ts, None, err, **k)
+    for bits in (6, 3):
+        wide = z(32, 64 * bits // 8)
+        calls[f"if{bits}_quantize"] = \
+            lambda bits=bits, wide=wide, **k: b.ifw_quantize(x, bits, 0, wide, s, ts, 0, err, **k)
+        calls[f"if{bits}_dequantize"] = \
+            lambda bits=bits, wide=wide, **k: b.ifw_dequantize(wide, s, ts, bits, y, **k)
+    return calls
+
+
+def binding():
+    from adaptive_block_scaled_b200 import build
+    build.build()
+    from adaptive_block_scaled_b200 import binding as b
+    return b
+
+
+NAMES = sorted(entries(None))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_host_tensors_are_refused(name):
+    with pytest.raises(ValueError, match="CUDA"):
+        entries(binding())[name]()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_run_on_the_tensors_device_and_the_given_stream(name, monkeypatch):
+    b = binding()
+    seen = []
+    monkeypatch.setattr(b, "_device", lambda n, *t: 3)
+    monkeypatch.setattr(b, "_call", lambda n, dev, stream, *a: seen.append((n, dev, stream, len(a))))
+    side = object()
+    entries(b)[name](stream=side)
+    assert seen == [(name, 3, side, len(getattr(b.lib, name).argtypes) - 1)]
+
+
+class Recorded:
+    """In place of torch.cuda.stream: whether a stream is current."""
+    def __init__(self):
+        self.now, self.inside = None, []
+
+    @contextlib.contextmanager
+    def stream(self, st):
+        self.now, before = st, self.now
+        yield
+        self.now = before
+
+
+def helpers(b):
+    x, ts = z(32, 64, dtype=BF16), z(1, dtype=F32)
+    q = (z(32, 32), z(32, 4), ts)
+    w = (z(64, 32), z(64, 4), ts)
+    wn, rstd, wide = z(64, dtype=F32), z(32, dtype=F32), z(32, 48)
+    return {
+        "quantize": lambda st: [b.quantize(x, m, stream=st) for m in ("if4", "nvfp4", "nvint4", "4over6")],
+        "quantize given ts": lambda st: b.quantize(x, "if4", ts, None, st),
+        "quantize_rht": lambda st: b.quantize_rht(x, 7, stream=st),
+        "quantize_w": lambda st: [b.quantize_w(x, n, stream=st) for n in (6, 3)],
+        "dequantize_w": lambda st: b.dequantize_w(wide, q[1], ts, 6, stream=st),
+        "quantize_fused": lambda st: [b.quantize_fused(x, stream=st),
+                                      b.quantize_fused(x, False, stream=st, signs=9)],
+        "quantize_fused_dequant": lambda st: b.quantize_fused_dequant(x, stream=st),
+        "dequantize": lambda st: b.dequantize(*q, stream=st),
+        "decode_f16": lambda st: b.decode_f16(*q[:2], stream=st),
+        "linear_nvfp4": lambda st: b.linear_nvfp4(q, w, stream=st),
+        "quantize_t": lambda st: b.quantize_t(x, "nvfp4", with_rows=True, stream=st),
+        "rms_norm_quantize": lambda st: b.rms_norm_quantize(x, wn, ts, residual=x, stream=st),
+        "rms_norm_backward": lambda st: b.rms_norm_backward(x, x, wn, rstd, stream=st),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(helpers(None)))
+def test_helpers_allocate_and_launch_on_the_given_stream(name, monkeypatch):
+    b, rec, side = binding(), Recorded(), object()
+    monkeypatch.setattr(torch.cuda, "stream", rec.stream)
+    monkeypatch.setattr(b, "_device", lambda n, *t: 0)
+    launches = []
+    monkeypatch.setattr(b, "_call", lambda n, dev, stream, *a: launches.append((rec.now, stream)))
+    made = []
+    for f in ("empty", "empty_like", "empty_strided", "zeros"):
+        real = getattr(torch, f)
+        monkeypatch.setattr(torch, f, lambda *a, real=real, **k: (made.append(rec.now), real(*a, **k))[1])
+    call = helpers(b)[name]
+    made.clear()
+    call(side)
+    # whatever the helper takes from the allocator comes under the stream, and the
+    # launch goes to the stream that is current then
+    assert launches and all(l == (side, None) for l in launches)
+    assert made and all(m is side for m in made)
+    launches.clear()
+    call(None)
+    assert launches and all(l == (None, None) for l in launches)
