@@ -140,11 +140,26 @@ def _device(name, *tensors):
     return dev
 
 
+def _same_device(stream, dev):
+    if stream.device_index != dev:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{dev}")
+
+
+def _under(stream, t):
+    """torch.cuda.stream(stream), a stream of t's device."""
+    _same_device(stream, t.get_device())
+    return torch.cuda.stream(stream)
+
+
 def _call(name, dev, stream, *args):
     """The C entry point `name` with args and the stream (the device's current
     one by default), with the tensors' device current."""
     fn = getattr(lib, name)
-    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        raw = _raw_stream(dev)
+    else:
+        _same_device(stream, dev)
+        raw = stream.cuda_stream
     if dev == torch.cuda.current_device():
         rc = fn(*args, raw)
     else:
@@ -465,7 +480,7 @@ def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
     """a, b: (codes, scales, ts) of NVFP4 operands [M, K] and [N, K].  Returns
     A B^T [M, N] of dtype."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, a[0]):
             return linear_nvfp4(a, b, dtype, err_flag)
     (M, kb), N, dev = a[0].shape, b[0].shape[0], a[0].device
     c = _new(M, N, dtype, dev)
@@ -530,7 +545,7 @@ def quantize_t(x, mode="if4", ts=None, with_rows=False, err_flag=None, stream=No
     codes_t, scales_t, ts) of x and of x^T under one tensor scale.  ts=None
     computes it; a float32 tensor is used as given."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return quantize_t(x, mode, ts, with_rows, err_flag)
     entry = _entry(mode, "quantize_t")
     if x.dim() != 2:
@@ -606,7 +621,7 @@ def rms_norm_quantize(x, weight, ts, residual=None, eps=1e-6, mode="if4", amax=N
     (x itself without a residual) and rstd [rows] are what rms_norm_backward
     takes.  amax: a float32 tensor raised to max |y|, for the next ts."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return rms_norm_quantize(x, weight, ts, residual, eps, mode, amax, err_flag)
     entry = _entry(mode, "rms_norm_quantize")
     if x.dim() != 2:
@@ -646,7 +661,7 @@ def rms_norm_backward(dy, h, weight, rstd, dres=None, stream=None):
     the gradient of the norm's output, and dres, that of h past the norm.
     Returns (dx, dweight): dx for x and the residual alike, dweight float32."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, dy):
             return rms_norm_backward(dy, h, weight, rstd, dres)
     (rows, cols), dev = h.shape, h.device
     dx, dweight = _new(rows, cols, h.dtype, dev), _new1(cols, torch.float32, dev)
@@ -696,7 +711,7 @@ def quantize_w(x, bits, mode=W_ADAPTIVE, ts=None, err_flag=None, stream=None):
     """IF6 (bits=6) or IF3 (bits=3) of a 2-D tensor, or the FP-only / INT-only
     candidate (mode).  Returns (codes, scales, ts); ts=None computes it."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return quantize_w(x, bits, mode, ts, err_flag)
     rows, cols, _ = _matrix(x, "x")
     dev = x.device
@@ -712,7 +727,7 @@ def quantize_w(x, bits, mode=W_ADAPTIVE, ts=None, err_flag=None, stream=None):
 
 def dequantize_w(codes, scales, ts, bits, dtype=torch.bfloat16, stream=None):
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, codes):
             return dequantize_w(codes, scales, ts, bits, dtype)
     rows, cols = scales.shape[0], scales.shape[1] * 16
     y = torch.empty((rows, cols), dtype=dtype, device=codes.device)
@@ -731,7 +746,7 @@ def quantize(x, mode="if4", ts=None, err_flag=None, stream=None):
     or "4over6".  Returns (codes, scales, ts).  ts=None computes the tensor
     scale; a float32 tensor is used as given."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return quantize(x, mode, ts, err_flag)
     rows, cols, _ = _matrix(x, "x")
     dev = x.device
@@ -750,7 +765,7 @@ def quantize(x, mode="if4", ts=None, err_flag=None, stream=None):
 def quantize_rht(x, signs, ts=None, err_flag=None, stream=None):
     """Random-sign Hadamard transform + IF4 quantize.  Returns (codes, scales, ts)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return quantize_rht(x, signs, ts, err_flag)
     rows, cols, _ = _matrix(x, "x")
     dev = x.device
@@ -801,7 +816,7 @@ def quantize_fused_dequant(x, with_nvfp4=True, sync_words=None, err_flag=None, s
     """The quantize-then-dequantize round trip in one launch.  Returns
     (codes, scales, ts, y) or (codes, scales, ts, nv_codes, nv_scales, y)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return quantize_fused_dequant(x, with_nvfp4, sync_words, err_flag)
     rows, cols, _ = _matrix(x, "x")
     dev = x.device
@@ -824,7 +839,7 @@ def quantize_fused(x, with_nvfp4=True, sync_words=None, err_flag=None, stream=No
     with signs, of its random-sign Hadamard transform.  Returns (codes,
     scales, ts) or (codes, scales, ts, nv_codes, nv_scales)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, x):
             return quantize_fused(x, with_nvfp4, sync_words, err_flag, signs=signs)
     rows, cols, _ = _matrix(x, "x")
     dev = x.device
@@ -841,7 +856,7 @@ def quantize_fused(x, with_nvfp4=True, sync_words=None, err_flag=None, stream=No
 
 def dequantize(codes, scales, ts, dtype=torch.bfloat16, stream=None):
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, codes):
             return dequantize(codes, scales, ts, dtype)
     rows, cols = codes.shape[0], codes.shape[1] * 2
     y = _new(rows, cols, dtype, codes.device)
@@ -851,7 +866,7 @@ def dequantize(codes, scales, ts, dtype=torch.bfloat16, stream=None):
 
 def decode_f16(codes, scales, stream=None):
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, codes):
             return decode_f16(codes, scales)
     rows, cols = codes.shape[0], codes.shape[1] * 2
     y = torch.empty((rows, cols), dtype=torch.float16, device=codes.device)

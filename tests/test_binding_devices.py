@@ -1,6 +1,7 @@
 """Which device and stream the binding's calls run on (no GPU needed: the C
 calls and the device lookup are replaced)."""
 import contextlib
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -128,7 +129,8 @@ def helpers(b):
 
 @pytest.mark.parametrize("name", sorted(helpers(None)))
 def test_helpers_allocate_and_launch_on_the_given_stream(name, monkeypatch):
-    b, rec, side = binding(), Recorded(), object()
+    b, rec = binding(), Recorded()
+    side = SimpleNamespace(device_index=-1)          # the device of host tensors
     monkeypatch.setattr(torch.cuda, "stream", rec.stream)
     monkeypatch.setattr(b, "_device", lambda n, *t: 0)
     launches = []
@@ -147,3 +149,21 @@ def test_helpers_allocate_and_launch_on_the_given_stream(name, monkeypatch):
     launches.clear()
     call(None)
     assert launches and all(l == (None, None) for l in launches)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_streams_of_another_device_are_refused(name, monkeypatch):
+    b = binding()
+    monkeypatch.setattr(b, "_device", lambda n, *t: 3)
+    with pytest.raises(ValueError, match="cuda:1.*cuda:3"):
+        entries(b)[name](stream=SimpleNamespace(device_index=1, cuda_stream=0))
+
+
+@pytest.mark.parametrize("name", sorted(helpers(None)))
+def test_helpers_refuse_streams_of_another_device(name, monkeypatch):
+    b, rec = binding(), Recorded()
+    monkeypatch.setattr(torch.cuda, "stream", rec.stream)
+    monkeypatch.setattr(b, "_device", lambda n, *t: 0)
+    monkeypatch.setattr(b, "_call", lambda *a: None)
+    with pytest.raises(ValueError, match="stream belongs to cuda:1"):
+        helpers(b)[name](SimpleNamespace(device_index=1))
