@@ -173,12 +173,25 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _rows(t, name, dtype=None, shape=None):
+    """A 2-D tensor whose rows are contiguous and do not overlap: its row
+    stride in elements."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be 2-D" + ("" if shape is None else f" of {tuple(shape)}"))
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return ld if rows > 1 and cols > 0 else cols
+
+
 def _matrix(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+    """Rows, columns and row stride of a 2-D tensor with contiguous rows that do
+    not overlap (an expanded tensor's rows do: its memory ends after the first)."""
+    ld = _rows(t, name)
+    return t.shape[0], t.shape[1], ld
 
 
 def _dtype(t, name):
@@ -416,20 +429,6 @@ def _dense(t, name, dtype, shape):
 def _word(t, name, dtype):
     if t is not None and (t.dtype is not dtype or t.numel() < 1):
         raise ValueError(f"{name} must be a {dtype} device tensor")
-
-
-def _rows(t, name, dtype=None, shape=None):
-    """A 2-D tensor whose rows are contiguous and do not overlap: its row
-    stride in elements."""
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be 2-D" + ("" if shape is None else f" of {tuple(shape)}"))
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return ld if rows > 1 and cols > 0 else cols
 
 
 def nvfp4_linear_workspace_bytes(M, N, K):

@@ -167,3 +167,26 @@ def test_helpers_refuse_streams_of_another_device(name, monkeypatch):
     monkeypatch.setattr(b, "_call", lambda *a: None)
     with pytest.raises(ValueError, match="stream belongs to cuda:1"):
         helpers(b)[name](SimpleNamespace(device_index=1))
+
+
+def test_overlapping_rows_are_refused(monkeypatch):
+    """An expanded tensor has the memory of one row: no call may take it for a
+    matrix of its shape, whether it reads or writes it."""
+    b = binding()
+    monkeypatch.setattr(b, "_device", lambda n, *t: 0)
+    monkeypatch.setattr(b, "_call", lambda *a: pytest.fail("the call went through"))
+    one = z(1, 64, dtype=BF16)
+    ts, c, s, sync = z(1, dtype=F32), z(32, 32), z(32, 4), z(64, dtype=torch.int32)
+    for x in (one.expand(32, 64), torch.as_strided(z(2048, dtype=BF16), (32, 64), (32, 1))):
+        for call in (lambda: b.if4_quantize(x, c, s, ts), lambda: b.if4_tensor_amax(x, ts),
+                     lambda: b.if4_quantize_rht(x, 1, c, s, ts), lambda: b.quantize(x),
+                     lambda: b.if4_quantize_fused(x, c, s, None, None, ts, sync),
+                     lambda: b.if4_dequantize(c, s, ts, x), lambda: b.quantize_w(x, 6),
+                     lambda: b.ifw_dequantize(z(32, 48), s, ts, 6, x)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+    seen = []
+    monkeypatch.setattr(b, "_call", lambda *a: seen.append(a))
+    b.if4_quantize(one, z(1, 32), z(1, 4), ts)
+    b.if4_quantize(z(64, 128, dtype=BF16)[::2, :64], c, s, ts)        # rows 256 apart
+    assert [a[5:8] for a in seen] == [(1, 64, 64), (32, 64, 256)]
