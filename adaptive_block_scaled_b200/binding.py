@@ -205,17 +205,40 @@ def _u8(t, name, shape):
         raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {tuple(shape)}")
 
 
+def _word(t, name, dtype):
+    if t is not None and (t.dtype is not dtype or t.numel() < 1):
+        raise ValueError(f"{name} must be a {dtype} device tensor")
+
+
+def _words(err_flag, **floats):
+    """float32 words and an int32 error word that a call reads or writes."""
+    for n, t in floats.items():
+        _word(t, n, torch.float32)
+    _word(err_flag, "err_flag", torch.int32)
+
+
+def _workspace(t, name="workspace"):
+    """Address and bytes of a workspace; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():             # an expanded one has less memory than elements
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 # ------------------------------------------------------- C entry points ---
 
 def if4_tensor_amax(x, amax, err_flag=None, stream=None):
     name = "if4_tensor_amax"
     rows, cols, ld = _matrix(x, "x")
+    _words(err_flag, amax=amax)
     _call(name, _device(name, x, amax, err_flag), stream, _ptr(x), _dtype(x, "x"), rows, cols, ld,
           _ptr(amax), _ptr(err_flag))
 
 
 def if4_tensor_scale(amax, ts, stream=None):
     name = "if4_tensor_scale"
+    _words(None, amax=amax, ts=ts)
     _call(name, _device(name, amax, ts), stream, _ptr(amax), _ptr(ts))
 
 
@@ -223,8 +246,7 @@ def _quantize_call(name, x, codes, scales, ts, ts_mode, err_flag, stream):
     rows, cols, ld = _matrix(x, "x")
     _u8(codes, "codes", (rows, cols // 2))
     _u8(scales, "scales", (rows, cols // 16))
-    if ts.dtype != torch.float32 or ts.numel() < 1:
-        raise ValueError("ts must be a float32 device tensor")
+    _words(err_flag, ts=ts)
     _call(name, _device(name, x, codes, scales, ts, err_flag), stream, _ptr(x), _dtype(x, "x"), rows,
           cols, ld, _ptr(codes), _ptr(scales), _ptr(ts), int(ts_mode), _ptr(err_flag))
 
@@ -240,6 +262,7 @@ def nvfp4_quantize(x, codes, scales, ts, ts_mode=TS_COMPUTE, err_flag=None, stre
 def if4_tensor_amax_rht(x, signs, amax, err_flag=None, stream=None):
     name = "if4_tensor_amax_rht"
     rows, cols, ld = _matrix(x, "x")
+    _words(err_flag, amax=amax)
     _call(name, _device(name, x, amax, err_flag), stream, _ptr(x), _dtype(x, "x"), rows, cols, ld,
           int(signs) & 0xFFFF, _ptr(amax), _ptr(err_flag))
 
@@ -249,6 +272,7 @@ def if4_quantize_rht(x, signs, codes, scales, ts, ts_mode=TS_COMPUTE, err_flag=N
     rows, cols, ld = _matrix(x, "x")
     _u8(codes, "codes", (rows, cols // 2))
     _u8(scales, "scales", (rows, cols // 16))
+    _words(err_flag, ts=ts)
     _call(name, _device(name, x, codes, scales, ts, err_flag), stream, _ptr(x), _dtype(x, "x"), rows,
           cols, ld, int(signs) & 0xFFFF, _ptr(codes), _ptr(scales), _ptr(ts), int(ts_mode),
           _ptr(err_flag))
@@ -263,8 +287,9 @@ def _fused_args(x, codes, scales, nv_codes, nv_scales, sync_words):
     if nv_codes is not None:
         _u8(nv_codes, "nv_codes", (rows, cols // 2))
         _u8(nv_scales, "nv_scales", (rows, cols // 16))
-    if sync_words.dtype != torch.int32 or sync_words.numel() < FUSED_SYNC_WORDS:
-        raise ValueError(f"sync_words must be an int32 device tensor of at least "
+    if (sync_words.dtype != torch.int32 or sync_words.numel() < FUSED_SYNC_WORDS
+            or not sync_words.is_contiguous()):
+        raise ValueError(f"sync_words must be a contiguous int32 device tensor of at least "
                          f"{FUSED_SYNC_WORDS} elements")
     return rows, cols, ld
 
@@ -274,6 +299,7 @@ def _fused_call(name, x, signs, codes, scales, nv_codes, nv_scales, ts, sync_wor
     """name (or its transform form, with signs) on 1/share of the device, or the
     whole of it for share=None."""
     rows, cols, ld = _fused_args(x, codes, scales, nv_codes, nv_scales, sync_words)
+    _words(err_flag, ts=ts)
     dev = _device(name, x, codes, scales, nv_codes, nv_scales, ts, sync_words, err_flag)
     _call(name, dev, stream, _ptr(x), _dtype(x, "x"), rows, cols, ld,
           *(() if signs is None else (int(signs) & 0xFFFF,)), _ptr(codes), _ptr(scales),
@@ -312,6 +338,7 @@ def if4_dequantize(codes, scales, ts, y, stream=None):
     rows, cols, ld = _matrix(y, "y")
     _u8(codes, "codes", (rows, cols // 2))
     _u8(scales, "scales", (rows, cols // 16))
+    _word(ts, "ts", torch.float32)
     _call(name, _device(name, codes, scales, ts, y), stream, codes.data_ptr(), scales.data_ptr(),
           ts.data_ptr(), rows, cols, y.data_ptr(), _dtype(y, "y"), ld)
 
@@ -336,6 +363,7 @@ def if4_gemm_f16(a, b, a_ts, b_ts, c, err_flag, stream=None):
             raise ValueError(f"{n} must be a contiguous float16 tensor")
     if b.shape[1] != K or tuple(c.shape) != (M, N) or c.dtype != torch.bfloat16:
         raise ValueError("shapes: a [M,K], b [N,K], c bf16 [M,N]")
+    _words(err_flag, a_ts=a_ts, b_ts=b_ts)
     _call(name, _device(name, a, b, a_ts, b_ts, c, err_flag), stream, _ptr(a), _ptr(b), _ptr(a_ts),
           _ptr(b_ts), M, N, K, _ptr(c), _ptr(err_flag))
 
@@ -361,9 +389,10 @@ def if4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, e
     name = "if4_linear"
     M, N = c.shape
     K = _linear_sizes(a_codes, a_scales, b_codes, b_scales, M, N, c)
+    _words(err_flag, a_ts=a_ts, b_ts=b_ts)
     dev = _device(name, a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c, err_flag)
     _call(name, dev, stream, _ptr(a_codes), _ptr(a_scales), _ptr(a_ts), _ptr(b_codes), _ptr(b_scales),
-          _ptr(b_ts), M, N, K, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(c),
+          _ptr(b_ts), M, N, K, *_workspace(workspace), _ptr(c),
           _ptr(err_flag))
 
 
@@ -374,6 +403,7 @@ def if4_linear_fused(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, c, err_fl
     name = "if4_linear_fused"
     M, N = c.shape
     K = _linear_sizes(a_codes, a_scales, b_codes, b_scales, M, N, c)
+    _words(err_flag, a_ts=a_ts, b_ts=b_ts)
     dev = _device(name, a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, c, err_flag)
     _call(name, dev, stream, _ptr(a_codes), _ptr(a_scales), _ptr(a_ts), _ptr(b_codes), _ptr(b_scales),
           _ptr(b_ts), M, N, K, _ptr(c), _ptr(err_flag))
@@ -386,6 +416,7 @@ def if4_linear_noalloc(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, c, err_
     name = "if4_linear_noalloc"
     M, N = c.shape
     K = _linear_sizes(a_codes, a_scales, b_codes, b_scales, M, N, c)
+    _words(err_flag, a_ts=a_ts, b_ts=b_ts)
     dev = _device(name, a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, c, err_flag)
     _call(name, dev, stream, _ptr(a_codes), _ptr(a_scales), _ptr(a_ts), _ptr(b_codes), _ptr(b_scales),
           _ptr(b_ts), M, N, K, _ptr(c), _ptr(err_flag))
@@ -398,10 +429,11 @@ def if4_linear_quantized(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, works
     K = _linear_sizes(a_codes, a_scales, b_codes, b_scales, M, N, c)
     _u8(c_codes, "c_codes", (M, N // 2))
     _u8(c_scales, "c_scales", (M, N // 16))
+    _words(err_flag, a_ts=a_ts, b_ts=b_ts, c_ts=c_ts)
     dev = _device(name, a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c_codes,
                   c_scales, c_ts, c, err_flag)
     _call(name, dev, stream, _ptr(a_codes), _ptr(a_scales), _ptr(a_ts), _ptr(b_codes), _ptr(b_scales),
-          _ptr(b_ts), M, N, K, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(c),
+          _ptr(b_ts), M, N, K, *_workspace(workspace), _ptr(c),
           _ptr(c_codes), _ptr(c_scales), _ptr(c_ts), _ptr(err_flag))
 
 
@@ -424,11 +456,6 @@ def _new1(n, dtype, device):
 def _dense(t, name, dtype, shape):
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-
-
-def _word(t, name, dtype):
-    if t is not None and (t.dtype is not dtype or t.numel() < 1):
-        raise ValueError(f"{name} must be a {dtype} device tensor")
 
 
 def nvfp4_linear_workspace_bytes(M, N, K):
@@ -458,7 +485,7 @@ def _nvfp4_linear(a, b, ws, c, err_flag, stream):
     if kb_b != kb:
         raise ValueError(f"a_codes has rows of {kb} bytes, b_codes of {kb_b}")
     _word(err_flag, "err_flag", torch.int32)
-    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    wp, wn = _workspace(ws)
     _call("nvfp4_linear", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), a_ts.data_ptr(),
           b_codes.data_ptr(), b_scales.data_ptr(), b_ts.data_ptr(), M, N, 2 * kb, wp, wn,
           c.data_ptr(), _dtype(c, "c"), _ptr(err_flag))
@@ -648,8 +675,7 @@ def if4_rms_norm_backward(dy, h, weight, rstd, dres, dx, dweight, workspace, str
     _norm_weight(weight, cols, dtype)
     _dense(rstd, "rstd", torch.float32, (rows,))
     _dense(dweight, "dweight", torch.float32, (cols,))
-    wp, wn = ((None, 0) if workspace is None else
-              (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+    wp, wn = _workspace(workspace)
     _call(name, dev, stream, dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, weight.data_ptr(),
           _dtype(weight, "weight"), rstd.data_ptr(), _ptr(dres), ld_dres, _dtype(h, "h"), rows, cols,
           dx.data_ptr(), ld_dx, dweight.data_ptr(), wp, wn)
@@ -690,8 +716,7 @@ def ifw_quantize(x, bits, mode, codes, scales, ts, ts_mode=TS_COMPUTE, err_flag=
     rows, cols, ld = _matrix(x, "x")
     _u8(codes, "codes", (rows, cols * bits // 8))
     _u8(scales, "scales", (rows, cols // 16))
-    if ts.dtype != torch.float32 or ts.numel() < 1:
-        raise ValueError("ts must be a float32 device tensor")
+    _words(err_flag, ts=ts)
     _call(name, _device(name, x, codes, scales, ts, err_flag), stream, _ptr(x), _dtype(x, "x"), rows,
           cols, ld, int(mode), _ptr(codes), _ptr(scales), _ptr(ts), int(ts_mode), _ptr(err_flag))
 
@@ -702,6 +727,7 @@ def ifw_dequantize(codes, scales, ts, bits, y, stream=None):
     rows, cols, ld = _matrix(y, "y")
     _u8(codes, "codes", (rows, cols * bits // 8))
     _u8(scales, "scales", (rows, cols // 16))
+    _word(ts, "ts", torch.float32)
     _call(name, _device(name, codes, scales, ts, y), stream, _ptr(codes), _ptr(scales), _ptr(ts),
           rows, cols, _ptr(y), _dtype(y, "y"), ld)
 
@@ -781,6 +807,7 @@ def quantize_rht(x, signs, ts=None, err_flag=None, stream=None):
 def _fused_dequant_call(name, x, codes, scales, nv_codes, nv_scales, ts, sync_words, y, share,
                         err_flag, stream):
     rows, cols, ld = _fused_dequant_args(x, codes, scales, nv_codes, nv_scales, sync_words, y)
+    _words(err_flag, ts=ts)
     dev = _device(name, x, codes, scales, nv_codes, nv_scales, ts, sync_words, y, err_flag)
     _call(name, dev, stream, _ptr(x), _dtype(x, "x"), rows, cols, ld, _ptr(codes), _ptr(scales),
           _ptr(nv_codes), _ptr(nv_scales), _ptr(ts), _ptr(sync_words), _ptr(y),

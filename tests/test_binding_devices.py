@@ -190,3 +190,54 @@ def test_overlapping_rows_are_refused(monkeypatch):
     b.if4_quantize(one, z(1, 32), z(1, 4), ts)
     b.if4_quantize(z(64, 128, dtype=BF16)[::2, :64], c, s, ts)        # rows 256 apart
     assert [a[5:8] for a in seen] == [(1, 64, 64), (32, 64, 256)]
+
+
+def refused(b, monkeypatch, match, *calls):
+    monkeypatch.setattr(b, "_device", lambda n, *t: 0)
+    monkeypatch.setattr(b, "_call", lambda *a: pytest.fail("the call went through"))
+    for call in calls:
+        with pytest.raises(ValueError, match=match):
+            call()
+
+
+def test_expanded_workspaces_are_refused(monkeypatch):
+    """Its elements count as bytes of memory that it does not have."""
+    b = binding()
+    ts, err = z(1, dtype=F32), z(1, dtype=torch.int32)
+    op, o = (z(32, 32), z(32, 4), ts, z(64, 32), z(64, 4), ts), z(32, 64, dtype=BF16)
+    y, rstd, wn = z(32, 64, dtype=BF16), z(32, dtype=F32), z(64, dtype=F32)
+    ws = z(1).expand(1 << 20)
+    refused(b, monkeypatch, "workspace must be contiguous",
+            lambda: b.nvfp4_linear(*op, ws, o, err),
+            lambda: b.if4_rms_norm_backward(y, y, wn, rstd, None, y, z(64, dtype=F32), ws),
+            lambda: b.if4_linear(*op, ws, o, err),
+            lambda: b.if4_linear_quantized(*op, ws, op[0], op[1], ts, o, err))
+    sync = z(1, dtype=torch.int32).expand(64)
+    x = z(32, 64, dtype=BF16)
+    refused(b, monkeypatch, "sync_words must be a contiguous",
+            lambda: b.if4_quantize_fused(x, op[0], op[1], None, None, ts, sync),
+            lambda: b.if4_quantize_fused_shared(x, op[0], op[1], None, None, ts, sync, 2),
+            lambda: b.if4_quantize_fused_dequant(x, op[0], op[1], None, None, ts, sync, y))
+
+
+def test_words_of_another_type_are_refused(monkeypatch):
+    """A float or an int that a kernel reads or writes through its address."""
+    b = binding()
+    x, c, s, y = z(32, 64, dtype=BF16), z(32, 32), z(32, 4), z(32, 64, dtype=BF16)
+    ts, sync, wide = z(1, dtype=F32), z(64, dtype=torch.int32), z(32, 48)
+    for bad in (z(1), z(1, dtype=torch.float64), z(0, dtype=F32)):
+        refused(b, monkeypatch, "ts|amax",
+                lambda: b.if4_tensor_amax(x, bad), lambda: b.if4_tensor_scale(ts, bad),
+                lambda: b.if4_tensor_scale(bad, ts), lambda: b.if4_tensor_amax_rht(x, 1, bad),
+                lambda: b.if4_quantize_rht(x, 1, c, s, bad), lambda: b.if4_quantize(x, c, s, bad),
+                lambda: b.if4_quantize_fused(x, c, s, None, None, bad, sync),
+                lambda: b.if4_quantize_fused_dequant(x, c, s, None, None, bad, sync, y),
+                lambda: b.if4_dequantize(c, s, bad, y), lambda: b.ifw_dequantize(wide, s, bad, 6, y),
+                lambda: b.ifw_quantize(x, 6, 0, wide, s, bad))
+    for bad in (z(1), z(1, dtype=torch.int64), z(0, dtype=torch.int32)):
+        refused(b, monkeypatch, "err_flag",
+                lambda: b.if4_tensor_amax(x, ts, bad), lambda: b.if4_quantize(x, c, s, ts, 0, bad),
+                lambda: b.if4_quantize_rht(x, 1, c, s, ts, 0, bad),
+                lambda: b.if4_quantize_fused(x, c, s, None, None, ts, sync, bad),
+                lambda: b.ifw_quantize(x, 6, 0, wide, s, ts, 0, bad),
+                lambda: b.if4_linear_fused(c, s, ts, c, s, ts, z(32, 32, dtype=BF16), bad))
