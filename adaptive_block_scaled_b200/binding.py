@@ -11,7 +11,8 @@ allocates its results and workspaces on it, as under torch.cuda.stream: they
 share no memory with what the current stream may still hand out.
 
 There is no fallback: if libif4.so is missing or a call fails, an exception
-is raised.
+is raised.  What only the device can see is reported in err_flag alone, an int32
+tensor that the caller zeroes and reads after the stream's work (DEV_* bits).
 """
 import ctypes
 import os
@@ -504,14 +505,18 @@ def nvfp4_linear(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, workspace, c,
 
 def linear_nvfp4(a, b, dtype=torch.bfloat16, err_flag=None, stream=None):
     """a, b: (codes, scales, ts) of NVFP4 operands [M, K] and [N, K].  Returns
-    A B^T [M, N] of dtype."""
+    A B^T [M, N] of dtype.
+
+    err_flag: an int32 tensor that the caller zeroes and reads.  Without one the
+    device's errors are lost: operands with INT4 groups (DEV_BAD_SCALE), or a wait
+    that ran out (DEV_TIMEOUT), then give an unspecified result in silence."""
     if stream is not None:
         with _under(stream, a[0]):
             return linear_nvfp4(a, b, dtype, err_flag)
     (M, kb), N, dev = a[0].shape, b[0].shape[0], a[0].device
     c = _new(M, N, dtype, dev)
     if err_flag is None:
-        err_flag = torch.zeros(1, dtype=torch.int32, device=dev)
+        err_flag = _new1(1, torch.int32, dev)        # nobody reads it
     need = lib.nvfp4_linear_workspace_bytes(M, N, 2 * kb)
     ws = _new1(need, torch.uint8, dev) if need else None
     _nvfp4_linear(a, b, ws, c, err_flag, None)

@@ -1,6 +1,8 @@
 """Which device and stream the binding's calls run on (no GPU needed: the C
 calls and the device lookup are replaced)."""
 import contextlib
+import os
+import re
 from types import SimpleNamespace
 
 import pytest
@@ -11,6 +13,9 @@ U8, F32, BF16 = torch.uint8, torch.float32, torch.bfloat16
 
 def z(*shape, dtype=U8):
     return torch.zeros(shape, dtype=dtype)
+
+
+U8_32, U8_4 = z(32, 32), z(32, 4)
 
 
 def entries(b):
@@ -241,3 +246,24 @@ def test_words_of_another_type_are_refused(monkeypatch):
                 lambda: b.if4_quantize_fused(x, c, s, None, None, ts, sync, bad),
                 lambda: b.ifw_quantize(x, 6, 0, wide, s, ts, 0, bad),
                 lambda: b.if4_linear_fused(c, s, ts, c, s, ts, z(32, 32, dtype=BF16), bad))
+
+
+def test_a_product_without_an_error_word_says_so_and_fills_none(monkeypatch):
+    b = binding()
+    assert "errors are lost" in " ".join(b.linear_nvfp4.__doc__.split())
+    ts = z(1, dtype=F32)
+    monkeypatch.setattr(b, "_device", lambda n, *t: 0)
+    seen = []
+    monkeypatch.setattr(b, "_call", lambda *a: seen.append(a))
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: pytest.fail("a kernel for a word nobody reads"))
+    b.linear_nvfp4((U8_32, U8_4, ts), (U8_32, U8_4, ts))
+    assert seen[0][0] == "nvfp4_linear" and seen[0][-1]          # an address, never NULL
+
+
+def test_the_readme_reads_its_error_word():
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                             "README.md")).read()
+    for block in re.findall(r"```python\n(.*?)```", text, flags=re.S):
+        calls = re.findall(r"linear_nvfp4\((?:[^()]|\([^()]*\))*\)", block)
+        assert all("err_flag=" in c for c in calls)
+        assert not calls or "err.item()" in block
