@@ -15,7 +15,9 @@
 //
 // Backward, with n = h * rstd the normalized row, g = dy * w:
 //   dx = RN(dres + rstd * (g - n * mean(g * n))),   dw = sum over rows of dy * n.
-// The quantizer passes gradients straight through.
+// The quantizer passes gradients straight through.  dw's sum over the rows, as
+// long as a batch, keeps more than binary32: each term n rounds once, a block's
+// sum of its rows is rounded once, and the sum of the blocks' once.
 
 #include <cuda_runtime.h>
 
@@ -477,8 +479,8 @@ rms_norm_quantize_kernel(const __grid_constant__ NormArgs a)
 
 // -------------------------------------------------------------- gradient ----
 
-constexpr int BACK_BLOCKS = 296;     // blocks that share the rows, and partial sums of dw
-constexpr int MAX_BACK_SMEM = 226 * 1024;   // a block's limit less its static arrays
+constexpr int BACK_BLOCKS = 296;     // partial sums of dw at most
+constexpr int BACK_THREADS = 512;
 
 struct BackArgs {
     const char *dy, *h, *w, *dres;
@@ -492,8 +494,36 @@ struct BackArgs {
     float inv_cols;
 };
 
-// The gradient's rows kernel works in units of 8 elements, so that dw of a
-// unit (8 floats), the weight and a row's inputs fit 64 registers.
+// Sums of dw over many rows: s + c is the sum, s its binary32 value and c what
+// s's additions rounded away.  With p = x * y exact, t = RN(s + p) and d = RN(s - t),
+// d + p is the rounding error of t whenever s - t is exact, which it is unless
+// |p| > |s| / 2; then d is off by at most 2^-24 |p|.  So a term costs at most one
+// rounding of its own size, and in a long sum almost none does, where a plain
+// chain's roundings are of the size of the sum.
+__device__ __forceinline__ void add_product(f2_t &s, f2_t &c, f2_t x, f2_t y)
+{
+    const f2_t t = f2_fma(x, y, s);
+    c = f2_add(c, f2_fma(x, y, f2_sub(s, t)));
+    s = t;
+}
+
+// s + c += s1 + c1, with the rounding error of s + s1 whatever their sizes.
+__device__ __forceinline__ void add_sums(f2_t &s, f2_t &c, f2_t s1, f2_t c1)
+{
+    const f2_t t = f2_add(s, s1), b = f2_sub(t, s);
+    const f2_t e = f2_add(f2_sub(s, f2_sub(t, b)), f2_sub(s1, b));
+    c = f2_add(c, f2_add(e, c1));
+    s = t;
+}
+
+// The sum, rounded once.  A c that is not finite says nothing: it comes from an
+// s that is Inf or NaN, or was on the way.
+__device__ __forceinline__ float sum_of(float s, float c)
+{
+    return fabsf(c) <= 3.402823466e38f ? __fadd_rn(s, c) : s;
+}
+
+// The gradient's rows kernel works in units of 8 elements.
 template <int DT>
 struct Unit {
     static constexpr int BYTES = 8 * elem_bytes<DT>();
@@ -514,32 +544,41 @@ __device__ __forceinline__ f2_t pair_of(const Unit<DT> &r, int j)
 
 template <int DT, int U>
 struct BackRing {
-    static constexpr int S = DT != DT_F32 && U == 1 ? 4 : 2;     // rows under way
+    static constexpr int S = DT != DT_F32 && U == 2 ? 4 : 2;     // rows under way
     static constexpr int BYTES = S * 3 * U * Unit<DT>::BYTES;    // per thread: h, dy, dres
 };
 
-// Rows of up to U * T units: one pass over dy, h and dres.  A block of
+// Rows of up to U * T units: one pass over dy, h and dres.  A block of 512 =
 // `slots` x T threads holds `slots` rows at a time, T threads each (a power of
 // two, at least a warp), with the next S rows of each slot under way in its
-// threads' rings; a thread keeps its columns' part of dw in registers over all
-// its rows.  The row sums meet at a barrier of the row's own threads.  At the
-// end the block's row slots add their parts through shared memory, and the
-// block writes one partial row.  Loads prefetched to registers, one row ahead,
-// spilled and left memory waits: 16384 x 4096 bf16 115 us.
+// threads' rings (192 KB, one block per SM); a thread keeps its columns' part of
+// dw in registers over all its rows, in twice binary32's precision.  The row sums
+// meet at a barrier of the row's own threads.  At the end the block's row slots
+// add their parts through shared memory, and the block writes one partial row of
+// binary32 values.
+//
+// The instructions bound it (16384 x 4096 bf16 87 to 92 us from board to board,
+// where memory needs 82): dw's sums are half as many again as the rest of its
+// arithmetic.  What two units per thread share of a row (its sum, barrier and
+// addresses) pays for them: one unit per thread took 101 (64 registers, 1024
+// threads per SM), and 126 with a row's inputs held in registers over the sum,
+// which spilled, instead of read from the ring again.  Above 8192 columns four
+// units, whose weight comes from L1 each time: 4096 x 12288 95 us, and 121 with
+// the weight in registers, which spilled.
 template <int DT, int WT, int U>
-__global__ void __launch_bounds__(U == 1 ? 1024 : 512, 1)
+__global__ void __launch_bounds__(BACK_THREADS, 1)
 rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
 {
     pdl_enter();
     using R = BackRing<DT, U>;
     constexpr int UP = elem_bytes<DT>() / 2;        // pieces of a unit
     __shared__ float sums[2][32];
-    extern __shared__ __align__(16) uint8_t back_smem[];   // the rings, then [slots - 1][cols]
+    extern __shared__ __align__(16) uint8_t back_smem[];   // the rings, then the slots' dw
     const int slots = blockDim.x / T, slot = threadIdx.x / T, t = threadIdx.x % T;
     const int warps = T >> 5, warp0 = slot * warps;
     const int units = a.gpr * 2;
     const int64_t step = (int64_t)gridDim.x * slots;
-    // the weight: in registers with one unit per thread, from L1 with more
+    // the weight: in registers with two units per thread, from L1 with four
     auto weight = [&](int u) {
         Unit<WT> r;
 #pragma unroll
@@ -552,12 +591,19 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
         }
         return r;
     };
-    const Unit<WT> w1 = weight(t);
-    f2_t dw[U][4];
+    Unit<WT> held[2];
+    if constexpr (U == 2)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) held[k] = weight(t + k * T);
+    auto weight_of = [&](int k) {
+        if constexpr (U == 2) return held[k];
+        else return weight(t + k * T);
+    };
+    f2_t dw[U][4], dc[U][4];
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dw[k][j] = f2_pack(0.0f, 0.0f);
+        for (int j = 0; j < 4; ++j) dw[k][j] = dc[k][j] = f2_pack(0.0f, 0.0f);
     // a warp's ring: [stage][h, dy, dres][unit of the lane][span of 32 units]
     constexpr uint32_t SPAN = 32 * Unit<DT>::BYTES;
     const int u0 = t & ~31;                         // the warp's first unit
@@ -591,7 +637,6 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
         ring_wait<R::S - 1>();
         const float rstd = rstd_next;
         if (row + step < a.rows) rstd_next = a.rstd[row + step];
-        // one unit stays in registers over the sum; more are read a second time
         Unit<DT> h, d, e;
         auto read = [&](int k, bool with_e) {
             const uint32_t r = ring + (stage * 3 * U + k) * SPAN;
@@ -604,17 +649,16 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (t + k * T < units) {
-                read(k, U == 1);
-                const Unit<WT> w = U == 1 ? w1 : weight(t + k * T);
+                read(k, false);
+                const Unit<WT> w = weight_of(k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // (n first: dy * h may leave binary32's range where dy * n does not)
                     const f2_t n = f2_mul(pair_of(h, j), RS), dy = pair_of(d, j);
-                    dw[k][j] = f2_fma(dy, n, dw[k][j]);
+                    add_product(dw[k][j], dc[k][j], dy, n);
                     acc = f2_fma(f2_mul(dy, pair_of(w, j)), n, acc);
                 }
             }
-        if constexpr (U == 1) fetch(row + R::S * step, stage);
         float s, hi;
         f2_unpack(acc, s, hi);
         s += hi;
@@ -637,8 +681,8 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
         for (int k = 0; k < U; ++k) {
             const int u = t + k * T;
             if (u < units) {
-                if constexpr (U > 1) read(k, true);
-                const Unit<WT> w = U == 1 ? w1 : weight(u);
+                read(k, true);
+                const Unit<WT> w = weight_of(k);
                 uint32_t o[DT == DT_F32 ? 8 : 4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -660,39 +704,48 @@ rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)
                     st_v4(p + 16 * q, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
         }
-        if constexpr (U > 1) fetch(row + R::S * step, stage);
+        fetch(row + R::S * step, stage);
         if (++stage == R::S) stage = 0;
     }
-    // the block's partial row: slot 0 adds the others' in order
+    // the block's partial row: the slots' parts added in order, two columns per
+    // thread, through the rings' memory (every copy has landed and been read; a
+    // thread's sums take 64 * U of its 192 * U bytes)
     const int cols = a.gpr * 16;
-    float *slot_dw = reinterpret_cast<float *>(back_smem + blockDim.x * R::BYTES);
-    if (slots > 1) {
-        if (slot > 0)
+    float *slot_s = reinterpret_cast<float *>(back_smem), *slot_c = slot_s + slots * cols;
+    float *out = a.part + (int64_t)blockIdx.x * cols;
+    auto put = [&](int at, f2_t s, f2_t c) {
+        float s0, s1, c0, c1;
+        f2_unpack(s, s0, s1);
+        f2_unpack(c, c0, c1);
+        *reinterpret_cast<f2_t *>(out + at) = f2_pack(sum_of(s0, c0), sum_of(s1, c1));
+    };
+    if (slots > 1) __syncthreads();
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int u = t + k * T;
-                if (u < units)
+    for (int k = 0; k < U; ++k) {
+        const int u = t + k * T;
+        if (u < units)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<f2_t *>(slot_dw + (slot - 1) * cols + u * 8 + 2 * j) = dw[k][j];
+            for (int j = 0; j < 4; ++j) {
+                const int at = u * 8 + 2 * j;
+                if (slots == 1) {
+                    put(at, dw[k][j], dc[k][j]);
+                } else {
+                    *reinterpret_cast<f2_t *>(slot_s + slot * cols + at) = dw[k][j];
+                    *reinterpret_cast<f2_t *>(slot_c + slot * cols + at) = dc[k][j];
+                }
             }
-        __syncthreads();
     }
-    if (slot == 0)
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int u = t + k * T;
-            if (u < units) {
-                for (int q = 0; q < slots - 1; ++q)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dw[k][j] = f2_add(dw[k][j], *reinterpret_cast<const f2_t *>(
-                                                        slot_dw + q * cols + u * 8 + 2 * j));
-                float *p = a.part + (int64_t)blockIdx.x * cols + u * 8;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) *reinterpret_cast<f2_t *>(p + 2 * j) = dw[k][j];
-            }
+    if (slots > 1) {
+        __syncthreads();
+        for (int at = 2 * threadIdx.x; at < cols; at += 2 * blockDim.x) {
+            f2_t s = *reinterpret_cast<const f2_t *>(slot_s + at);
+            f2_t c = *reinterpret_cast<const f2_t *>(slot_c + at);
+            for (int q = 1; q < slots; ++q)
+                add_sums(s, c, *reinterpret_cast<const f2_t *>(slot_s + q * cols + at),
+                         *reinterpret_cast<const f2_t *>(slot_c + q * cols + at));
+            put(at, s, c);
         }
+    }
 }
 
 // More columns than the rows kernel holds: dx with a block per row, dy and h
@@ -755,56 +808,71 @@ rms_norm_dx_kernel(const __grid_constant__ BackArgs a)
     }
 }
 
-// Partial sums of dw: block (i, c) adds rows i, i + n, ... for 256 columns.
+// Partial sums of dw: block (i, c) adds rows i, i + n, ... for 512 columns, two
+// per thread.
 template <int DT>
 __global__ void __launch_bounds__(256)
 rms_norm_dw_kernel(const __grid_constant__ BackArgs a)
 {
     pdl_enter();
     constexpr int ES = elem_bytes<DT>();
-    const int col = blockIdx.y * 256 + threadIdx.x;
+    const int col = (blockIdx.y * 256 + threadIdx.x) * 2;
     if (col >= a.gpr * 16) return;
-    auto value = [&](const char *p) {
-        if constexpr (DT == DT_F32)
-            return *reinterpret_cast<const float *>(p);
-        else if constexpr (DT == DT_BF16)
-            return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short *>(p) << 16);
-        else
-            return __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short *>(p)));
+    auto pair = [&](const char *p) {
+        if constexpr (DT == DT_F32) {
+            const float2 v = *reinterpret_cast<const float2 *>(p);
+            return f2_pack(v.x, v.y);
+        } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+            return DT == DT_BF16 ? f2_from_bf16x2(v) : f2_pack(f16lo_to_f32(v), f16hi_to_f32(v));
+        }
     };
-    float s = 0.0f;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x)
-        s = fmaf(value(a.dy + row * a.ld_dy + (int64_t)col * ES),
-                 value(a.h + row * a.ld_h + (int64_t)col * ES) * a.rstd[row], s);
-    a.part[(int64_t)blockIdx.x * a.gpr * 16 + col] = s;
+    f2_t s = f2_pack(0.0f, 0.0f), c = s;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float rstd = a.rstd[row];
+        add_product(s, c, pair(a.dy + row * a.ld_dy + (int64_t)col * ES),
+                    f2_mul(pair(a.h + row * a.ld_h + (int64_t)col * ES), f2_pack(rstd, rstd)));
+    }
+    float s0, s1, c0, c1;
+    f2_unpack(s, s0, s1);
+    f2_unpack(c, c0, c1);
+    *reinterpret_cast<f2_t *>(a.part + (int64_t)blockIdx.x * a.gpr * 16 + col) =
+        f2_pack(sum_of(s0, c0), sum_of(s1, c1));
 }
 
-// dw: n <= BACK_BLOCKS partial rows.  A block takes 32 columns; warp v adds rows
-// v, v + 32, ..., all loaded before they are added, then one warp adds the 32
-// sums in order.
+// dw: n <= BACK_BLOCKS partial rows, added in binary64 and rounded once.  A block
+// takes 32 columns; warp v adds rows v, v + 32, ..., all loaded before they are
+// added, then one warp adds the warps' sums.  Few rows take little of its code: a
+// straight line of 41 additions cost a single row 1 us.
 __global__ void __launch_bounds__(1024)
 rms_norm_dw_sum_kernel(const float *part, int n, int cols, float *dw)
 {
     pdl_enter();
-    __shared__ float sums[32][33];
+    __shared__ double sums[32][33];
     constexpr int PER = (BACK_BLOCKS + 31) / 32;
     const int lane = threadIdx.x & 31, v = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
-    float x[PER];
+    const float *p = part + (int64_t)v * cols + col;
+    const bool in = col < cols;
+    double s = in && v < n ? (double)ld_after_wait(p) : 0.0;
+    if (n > 32) {
+        float x[PER - 1];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        x[i] = col < cols && v + 32 * i < n ? ld_after_wait(part + (int64_t)(v + 32 * i) * cols + col)
-                                            : 0.0f;
-    float s = x[0];
+        for (int i = 0; i < PER - 1; ++i)
+            x[i] = in && v + 32 * (i + 1) < n ? ld_after_wait(p + (int64_t)(i + 1) * 32 * cols) : 0.0f;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) s = __fadd_rn(s, x[i]);
+        for (int i = 0; i < PER - 1; ++i) s = __dadd_rn(s, (double)x[i]);
+    }
     sums[v][lane] = s;
     __syncthreads();
-    if (v == 0 && col < cols) {
-        s = 0.0f;
+    if (v == 0 && in) {
+        const int m = (min(n, 32) + 3) & ~3;
+        double y[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 1
+        for (int i = 0; i < m; i += 4)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += sums[i][lane];
-        dw[col] = s;
+            for (int k = 0; k < 4; ++k) y[k] = __dadd_rn(y[k], sums[i + k][lane]);
+        dw[col] = (float)__dadd_rn(__dadd_rn(y[0], y[1]), __dadd_rn(y[2], y[3]));
     }
 }
 
@@ -961,26 +1029,25 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
     return by_types(x_dtype, w_dtype, [&](auto dt, auto wt) {
         constexpr int DT = decltype(dt)::value, WT = decltype(wt)::value;
         if (n <= (DT == DT_F32 ? 512 : 1024)) {
-            // up to 8192 columns one unit per thread, blocks of 512 threads (two
-            // per SM) or, above 4096 columns, 1024; then 512 threads, four units
+            // the fewest threads per row (a power of two) that hold it, two units
+            // each up to 8192 columns, four above
             const int64_t units = 2 * n;
+            const int per = units <= 1024 ? 2 : 4;
             int T = 32;
-            while (T < 1024 && T < units) T *= 2;
-            if (units > 1024) T = 512;
-            const int threads = std::max(T, 512), slots = threads / T;
-            const int parts = (int)std::min<int64_t>((rows + slots - 1) / slots,
-                                                     units > 512 ? BACK_BLOCKS / 2 : BACK_BLOCKS);
+            while (T * per < units) T *= 2;
+            const int slots = BACK_THREADS / T;
+            const int parts = (int)std::min<int64_t>((rows + slots - 1) / slots, BACK_BLOCKS / 2);
             auto rows_kernel = [&](auto V) {
                 constexpr int U = decltype(V)::value;
                 auto kernel = rms_norm_backward_rows_kernel<DT, WT, U>;
                 static OncePerDevice done;
-                const int ok = allow_smem(kernel, MAX_BACK_SMEM, d, done);
+                constexpr int SMEM = BACK_THREADS * BackRing<DT, U>::BYTES;
+                const int ok = allow_smem(kernel, SMEM, d, done);
                 if (ok != IF4_OK) return ok;
                 cudaLaunchConfig_t cfg = {};
                 cfg.gridDim = dim3((unsigned)parts, 1, 1);
-                cfg.blockDim = dim3((unsigned)threads, 1, 1);
-                cfg.dynamicSmemBytes = (size_t)threads * BackRing<DT, U>::BYTES +
-                                       (size_t)(slots - 1) * (size_t)cols * sizeof(float);
+                cfg.blockDim = dim3(BACK_THREADS, 1, 1);
+                cfg.dynamicSmemBytes = SMEM;
                 cfg.stream = st;
                 cudaLaunchAttribute attr[1];
                 attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -990,17 +1057,17 @@ int if4_rms_norm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t 
                 return launched(cudaLaunchKernelEx(&cfg, kernel, a, T));
             };
             int r;
-            if constexpr (DT != DT_F32)
-                r = units <= 1024 ? rows_kernel(std::integral_constant<int, 1>{})
-                                  : rows_kernel(std::integral_constant<int, 4>{});
+            if constexpr (DT == DT_F32)
+                r = rows_kernel(std::integral_constant<int, 2>{});
             else
-                r = rows_kernel(std::integral_constant<int, 1>{});
+                r = per == 2 ? rows_kernel(std::integral_constant<int, 2>{})
+                             : rows_kernel(std::integral_constant<int, 4>{});
             if (r != IF4_OK) return r;
             return sum_dw(parts);
         }
         const int parts = (int)std::min<int64_t>(rows, BACK_BLOCKS);
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)parts, (unsigned)((cols + 255) / 256), 1);
+        cfg.gridDim = dim3((unsigned)parts, (unsigned)((cols + 511) / 512), 1);
         cfg.blockDim = dim3(256, 1, 1);
         cfg.stream = st;
         int r = launched(cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel<DT>, a));

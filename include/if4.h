@@ -445,8 +445,9 @@ int nvfp4_rms_norm_quantize(const void *x, int64_t ld_x, const void *residual, i
  * dx is the gradient of x and of the residual alike.  dres, the gradient that
  * reaches h past the norm, may be NULL.  dy, h, dres, dx [rows, cols] of
  * x_dtype; h and rstd as the forward call wrote them; dweight float [cols],
- * overwritten (zero for rows == 0).  Sums in binary32, in an order that does
- * not change between calls.  dx may be dy's or dres's own memory (with the
+ * overwritten (zero for rows == 0).  The mean's sum is binary32; dweight's sum
+ * over the rows is off by at most half a step of dweight plus 3 * 2^-24 of the
+ * sum of |dy * n|.  The order of the additions does not change between calls.  dx may be dy's or dres's own memory (with the
  * same row stride).  workspace: if4_rms_norm_backward_workspace_bytes (0 for
  * invalid sizes), 256-byte aligned, one per call that may run at the same
  * time.  Types, alignment and strides as the forward call.
