@@ -1321,7 +1321,8 @@ int launch_linear(const Problem &p, const DeviceInfo &d)
 extern "C" size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > MAX_MN || N > MAX_MN || K > MAX_K) return 0;
-    // the narrowest tile width needs the most blocks
+    // B in tiles of 240 columns, two blocks each; tiles of 128 columns, one block
+    // each, never need more: 2 ceil(N / 240) >= ceil(N / 128)
     return use_pair(M, N, K) ? packed_bytes((M + 255) / 256 * 2 + (N + 239) / 240 * 2, K) : 0;
 }
 
