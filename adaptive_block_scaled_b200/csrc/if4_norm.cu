@@ -292,8 +292,9 @@ __device__ __forceinline__ void load_h(const NormArgs &a, int64_t row, int g, Ra
 // time).  A block takes rows blockIdx.x, + gridDim.x, ...; PREFETCH: the next
 // row's loads are issued as soon as h of a row is formed.
 //
-// The encoder's and the norm's instructions bound it as much as memory does
-// (IF4 8192 x 8192 bf16: about 400 per group), so two groups per thread, which
+// The encoder's and the norm's instructions bound it as much as memory does (IF4
+// 8192 x 8192 bf16: 402 per group, 61 % of the issue slots with DRAM 59 % busy;
+// NVFP4 280, 54 and 73 %), so two groups per thread, which
 // share the row's sum, with loads straight to registers (128 of them, 512
 // threads per SM) beat one group (64 registers, 1024 threads: 92 us) and rows
 // under way in shared memory (85 us).
@@ -557,14 +558,15 @@ struct BackRing {
 // add their parts through shared memory, and the block writes one partial row of
 // binary32 values.
 //
-// The instructions bound it (16384 x 4096 bf16 87 to 92 us from board to board,
-// where memory needs 82): dw's sums are half as many again as the rest of its
-// arithmetic.  What two units per thread share of a row (its sum, barrier and
-// addresses) pays for them: one unit per thread took 101 (64 registers, 1024
-// threads per SM), and 126 with a row's inputs held in registers over the sum,
-// which spilled, instead of read from the ring again.  Above 8192 columns four
-// units, whose weight comes from L1 each time: 4096 x 12288 95 us, and 121 with
-// the weight in registers, which spilled.
+// Memory (73 % busy) and its instructions (195 per unit, 57 % of the issue slots)
+// bound it together: 16384 x 4096 bf16 87 to 94 us from board to board, where memory
+// needs 82.  dw's sums take four of the seven arithmetic instructions per pair of
+// columns in front of the row's sum.  What two units per thread share of a row (its
+// sum, barrier and addresses) pays for them: one unit per thread took 101 (64
+// registers, 1024 threads per SM), and 126 with a row's inputs held in registers
+// over the sum, which spilled, instead of read from the ring again.  Above 8192
+// columns four units, whose weight comes from L1 each time: 4096 x 12288 95 us, and
+// 121 with the weight in registers, which spilled.
 template <int DT, int WT, int U>
 __global__ void __launch_bounds__(BACK_THREADS, 1)
 rms_norm_backward_rows_kernel(const __grid_constant__ BackArgs a, int T)

@@ -877,8 +877,8 @@ quantize_fused_kernel(const char *__restrict__ x, int64_t ld_bytes, uint32_t gpr
 // 16-bit outputs: the unit-scale fp16 decode (the linear's operands) uses the
 // byte-permute group decode, the dequantizer with a tensor scale the
 // per-element table; on 134 MB tensors each is the faster of the two for its
-// kernel (fp16 decode 31.3 against 31.7 us, bf16 dequantize 29.4 against
-// 31.5 us).
+// kernel (fp16 decode 31.3 against 31.7 us, and 32.5 since its loads stay behind
+// the launch wait; bf16 dequantize 29.4 against 31.5 us).
 template <int ODT, bool UNIT_TS, bool V8>
 __global__ void __launch_bounds__(256)
 dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,

@@ -18,11 +18,10 @@
 // The column codes are put back in order through shared memory, so that a
 // tile's code bytes of a column leave as one run.
 //
-// With both forms and IF4 the encoder's instructions bound it (two encodes of
-// about 200 instructions per 16 values, 270 in all): 8192 x 8192 bf16 with the
-// tensor scale given takes 74 us, four blocks per SM issuing in 82 % of the
-// cycles.  Holding the tile's loads in registers instead allowed two: 83 us.
-// NVFP4 takes 46 us (about 145 instructions).
+// With both forms the encoder's instructions bound it: 511 per 16 values in IF4
+// (two encodes and all around them), 281 in NVFP4.  8192 x 8192 bf16 with the tensor
+// scale given takes 74 and 46 to 47 us, four blocks per SM issuing in 81 and 78 % of
+// the cycles.  Holding the tile's loads in registers instead allowed two: IF4 83 us.
 
 #include <cuda_runtime.h>
 

@@ -303,10 +303,12 @@ nvfp4_linear_few(const uint8_t *x_codes, const uint8_t *x_scales, const float *x
 // distributed shared memory, each for its share of the tokens: no workspace,
 // no atomics, the same sum every time.
 //
-// About 3.5 us of it is launch, tensor memory and the first loads' latency, 1.2
-// the reduction, and the rest the operands' way from L2, at about 8 TB/s: 256 x
-// 256 x 512 3.6 us, 48 x 8192 x 4096 9.2, 100 x 4096 x 14336 14.9.  (Scales loaded
-// two, three or four units ahead instead of one: 1 to 10 % slower.)
+// One tile and one unit of K (16 x 128 x 512) take 3.4 us: launch, tensor memory,
+// the first loads' latency and the epilogue.  A cluster's reduction adds 0.8 (16
+// x 128 x 1024 to 4096 4.2 to 4.3).  Above that a CTA waits for its own chain of
+// loads: 48 x 8192 x 4096 takes 9.2 us with DRAM 17 %, L2 16 % and the tensor pipe
+// 5 % busy, 100 x 4096 x 14336 14.9.  (Scales loaded two, three or four units ahead
+// instead of one: 1 to 10 % slower.)
 
 namespace split {
 
@@ -615,10 +617,13 @@ nvfp4_linear_split(const __grid_constant__ CUtensorMap tmap_w,
 // per product; narrow ones use more SMs when there are few tiles.  Measured, BN =
 // 240 against 128, us: 8192 x 4096 x 4096 68.6 / 86.5, 1024 x 4096 x 4096
 // 12.7 / 15.8 (72 and 128 tiles), 512 x 4096 x 4096 11.9 / 11.5 (36 and 64),
-// 1001 x 1555 x 4128 22.0 / 16.6 (28 and 52): 128 while its tiles fit the pairs.
+// 1001 x 1555 x 4128 22.0 / 16.6 (28 and 52; 13.8 with the stores of flush_pairs): 128
+// while its tiles fit the pairs.
 //
-// Long runs are bound by the board's power: 8192 x 4096 x 4096 takes 58 us in
-// bursts and 69 us when repeated for 0.1 s.
+// Long runs are bound by the board's power: 8192 x 4096 x 4096 takes 58 us in bursts
+// of 1.2 ms at 1965 MHz, and 67 us over 3 s, at 1500 MHz and 985 W with sw_power_cap
+// the one active reason.  binary32 C takes 84: its rows leave as each lane's own
+// stores, not as boxes.
 
 namespace duo {
 
@@ -1306,8 +1311,8 @@ int launch_linear(const Problem &p, const DeviceInfo &d)
     // / 32 / 64 tokens per CTA: 32 x 4096 x 4096 6.5 / 7.3 / 7.4, 128 x 2048 x 2048
     // 6.4 / 6.8 / 8.1 (512 units each with 16); 64 x 4096 x 4096 8.1 / 7.7 / 9.4
     // (1024 with 16), 128 x 8192 x 4096 19.4 / 10.9 / 11.3 (2048 with 32); 128 x
-    // 4096 x 14336 23.5 / 16.9 / 14.0 (3584 with 32), 128 x 14336 x 4096 35.3 /
-    // 20.6 / 12.9.  And one wave whatever K is: 4096 x 256 x 512 8.4 / 4.9 / 6.1.
+    // 4096 x 14336 23.5 / 16.9 / 15.1 (3584 with 32), 128 x 14336 x 4096 35.3 /
+    // 20.6 / 14.2.  And one wave whatever K is: 4096 x 256 x 512 8.4 / 4.9 / 6.1.
     auto suits = [&](int nt, int64_t most) {
         return p.M <= nt || (tiles(nt) <= slots && tiles(nt) * units <= most);
     };
