@@ -42,9 +42,8 @@ __device__ __forceinline__ void load_group(const char *p, Raw<DT> &r)
     }
 }
 
-// The same for values that an earlier kernel of the stream may have written, or
-// that this kernel overwrites itself: coherent, and not moved in front of
-// pdl_enter().  v8: 32-byte aligned, 256 bits at once.
+// The same with the width chosen at run time, also for values that this kernel
+// overwrites itself.  v8: 32-byte aligned, 256 bits at once.
 template <int DT>
 __device__ __forceinline__ void load_group_rw(const char *p, Raw<DT> &r, bool v8)
 {

@@ -12,7 +12,7 @@ def B():
 
 
 @pytest.mark.parametrize("captured", [False, True])
-@pytest.mark.parametrize("M", [1, 2, 48, 300])
+@pytest.mark.parametrize("M", [1, 2, 48, 300, 1300])      # (1300: CTA pairs in all but the first)
 @pytest.mark.parametrize("N,K", [(256, 512), (2048, 2048), (1032, 1056)])
 def test_norm_and_product_over_the_same_buffers(M, N, K, captured):
     bb = B()
@@ -115,3 +115,49 @@ def test_quantizers_and_dequantizers_over_the_same_buffers(rows, cols, captured)
         torch.cuda.synchronize()
         for o, k in zip(outs, want):
             assert torch.equal(o, k)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 256), (16, 4096), (200, 2048), (40, 12288), (5, 33024)])
+def test_norm_and_gradient_with_a_weight_just_written(rows, cols, captured):
+    """Each round decodes another weight into the same buffer, then the norm and
+    its gradient read it."""
+    bb = B()
+    g = torch.Generator().manual_seed(rows + cols)
+    rounds = 8
+    x = torch.randn((rows, cols), generator=g).bfloat16().cuda()
+    dy = torch.randn((rows, cols), generator=g).bfloat16().cuda()
+    ws = [bb.quantize((1 + 0.1 * torch.randn((1, cols), generator=g)).bfloat16().cuda())
+          for _ in range(rounds)]
+    ts = torch.tensor([0.01], device="cuda")
+    w = torch.empty((1, cols), dtype=torch.bfloat16, device="cuda")
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty((rows, cols // 2), **u8), torch.empty((rows, cols // 16), **u8),
+             torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda"),
+             torch.empty(cols, device="cuda")) for _ in range(rounds)]
+    rstd = torch.empty(rows, device="cuda")
+    work = torch.empty(bb.if4_rms_norm_backward_workspace_bytes(rows, cols), **u8)
+
+    def run(sync=lambda: None):
+        for q, (codes, scales, dx, dw) in zip(ws, outs):
+            bb.if4_dequantize(*q, w)
+            sync()
+            bb.if4_rms_norm_quantize(x, None, w[0], 1e-6, None, rstd, codes, scales, ts)
+            sync()
+            bb.if4_rms_norm_backward(dy, x, w[0], rstd, None, dx, dw, work)
+            sync()
+
+    run(torch.cuda.synchronize)
+    want = [tuple(t.clone() for t in o) for o in outs]
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(4):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        for o, k in zip(outs, want):
+            assert all(torch.equal(p, q) for p, q in zip(o, k))
