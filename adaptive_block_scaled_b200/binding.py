@@ -218,12 +218,12 @@ def _words(err_flag, **floats):
     _word(err_flag, "err_flag", torch.int32)
 
 
-def _workspace(t, name="workspace"):
+def _workspace(t):
     """Address and bytes of a workspace; (None, 0) for None."""
     if t is None:
         return None, 0
     if not t.is_contiguous():             # an expanded one has less memory than elements
-        raise ValueError(f"{name} must be contiguous")
+        raise ValueError("workspace must be contiguous")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
@@ -486,7 +486,7 @@ def _nvfp4_linear(a, b, ws, c, err_flag, stream):
     if kb_b != kb:
         raise ValueError(f"a_codes has rows of {kb} bytes, b_codes of {kb_b}")
     _word(err_flag, "err_flag", torch.int32)
-    wp, wn = _workspace(ws)
+    wp, wn = (None, 0) if ws is None else _workspace(ws)
     _call("nvfp4_linear", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), a_ts.data_ptr(),
           b_codes.data_ptr(), b_scales.data_ptr(), b_ts.data_ptr(), M, N, 2 * kb, wp, wn,
           c.data_ptr(), _dtype(c, "c"), _ptr(err_flag))
